@@ -92,6 +92,8 @@ def lib():
                     fn = getattr(L, name)
                     fn.argtypes = args
                     fn.restype = ctypes.c_int
+                L.lora_kv_attention_workspace.argtypes = [ctypes.POINTER(mlora_kv_cache), _I32]
+                L.lora_kv_attention_workspace.restype = ctypes.c_int64
                 L.lora_error_string.argtypes = [ctypes.c_int]
                 L.lora_error_string.restype = ctypes.c_char_p
                 L.lora_abi_version.restype = ctypes.c_int
@@ -325,3 +327,11 @@ def lora_test_set_wait_limit_ns(limit_ns: int) -> None:
 
 def abi_version() -> int:
     return int(lib().lora_abi_version())
+
+
+# the operators around the adapted projections (they extend SIGNATURES)
+from .serve import (  # noqa: E402
+    ERR_WORKSPACE, KV_MAX_HEAD_DIM, KV_MAX_REQUESTS, MLORA_FP32, STATUS_BAD_LENGTH, STATUS_BAD_REQUEST,
+    STATUS_BAD_TOKEN, STATUS_NO_PAGES, KvAppend, KvAttention, KvBatch, KvCache, LogitsAdjust, Rope,
+    kv_attention_workspace, lora_kv_append, lora_kv_attention, lora_kv_attention_workspace, lora_kv_layout,
+    lora_logits_adjust, make_kv_cache, mlora_kv_attn, mlora_kv_batch, mlora_kv_cache, mlora_kv_rows, mlora_logits)

@@ -14,6 +14,7 @@
 
 #include "launch.h"
 #include "mlora.h"
+#include "serve.h"
 
 namespace {
 
@@ -30,6 +31,14 @@ int cuda_fail(cudaError_t e, const char *where) {
   snprintf(g_cuda_err, sizeof(g_cuda_err), "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
   return MLORA_ERR_CUDA;
 }
+
+}  // namespace
+
+// The same error text and launch count for the entry points of serve_api.cu.
+int mlora::api_cuda_fail(cudaError_t e, const char *where) { return cuda_fail(e, where); }
+void mlora::api_count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+
+namespace {
 
 // Checks a pool descriptor for the phases a call runs.
 int check_pool(const mlora_pool *p, int32_t layer, bool need_a, bool need_b) {
@@ -539,6 +548,7 @@ const char *lora_error_string(int code) {
     case MLORA_ERR_POOL: return "malformed adapter pool descriptor";
     case MLORA_ERR_CUDA: return g_cuda_err;
     case MLORA_ERR_TOO_LARGE: return "num_rows * r_max exceeds the built-in scratch (MLORA_NOALLOC_MAX_FLOATS)";
+    case MLORA_ERR_WORKSPACE: return "the workspace is smaller than the call needs";
     default: return "unknown error code";
   }
 }

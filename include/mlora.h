@@ -98,6 +98,7 @@ extern "C" {
 #define MLORA_ERR_POOL (-5)        /* malformed pool descriptor */
 #define MLORA_ERR_CUDA (-6)        /* a CUDA call failed; see lora_error_string(MLORA_ERR_CUDA) */
 #define MLORA_ERR_TOO_LARGE (-7)   /* the call needs more than the built-in scratch of lora_sgmv_noalloc */
+#define MLORA_ERR_WORKSPACE (-8)   /* the workspace is smaller than the call needs */
 
 /* Device status bits, OR-ed into *dev_status. */
 #define MLORA_STATUS_BAD_OFFSETS 1
@@ -105,8 +106,12 @@ extern "C" {
 #define MLORA_STATUS_BAD_RANK 4
 #define MLORA_STATUS_BAD_PAGE 8
 #define MLORA_STATUS_TIMEOUT 16
+#define MLORA_STATUS_NO_PAGES 32      /* lora_kv_layout: more pages needed than are free */
+#define MLORA_STATUS_BAD_LENGTH 64    /* a length, a position or the free ring's state is out of range */
+#define MLORA_STATUS_BAD_TOKEN 128    /* lora_logits_adjust: a token id outside the vocabulary */
+#define MLORA_STATUS_BAD_REQUEST 256  /* a row's request outside [0, num_requests) */
 
-typedef enum { MLORA_BF16 = 0, MLORA_FP16 = 1 } mlora_dtype;
+typedef enum { MLORA_BF16 = 0, MLORA_FP16 = 1, MLORA_FP32 = 2 /* lora_logits_adjust only */ } mlora_dtype;
 typedef enum { MLORA_POOL_STACKED = 0, MLORA_POOL_PAGED = 1 } mlora_pool_kind;
 
 /* One adapter pool for one projection shape (d_in -> d_out), every layer, every slot.
@@ -271,6 +276,189 @@ typedef struct {
 
 MLORA_API int lora_sgmv_sequence(const mlora_group *groups, int32_t num_groups, uint32_t flags, int32_t *dev_status,
                                  void *stream);
+
+/* ---- the step around the adapters: cache layout, append, attention, logits -----------------
+ * A decode or mixed step of many tenants' requests, besides the adapted projections: where each new
+ * row goes in a paged key-value cache, the write of its k and v, the attention that reads the
+ * cache, and each request's own adjustment of its logits. The paged cache is S-LoRA's (section 3,
+ * "Unified Paging": the key-value pages live in the same pool as the adapters' pages, one list of
+ * free pages); any strided view of one allocation serves, an adapter pool's `pages` included.
+ *
+ * The calls share the conventions above, and these:
+ *   - Each takes a host struct that may be built once and used for every step (the lengths are in
+ *     device memory, so a captured graph can be replayed). num_rows is the capacity of the row
+ *     arrays; a row that stands for nothing has -1 as its request, position and cache slot, and no
+ *     call reads or writes anything for it but where said.
+ *   - Every kernel waits for the work before it in the stream before it reads or writes any memory,
+ *     whether or not it was launched programmatically. */
+
+#define MLORA_KV_MAX_REQUESTS 8192
+#define MLORA_KV_MAX_HEAD_DIM 256
+
+/* lora_kv_layout: from the requests' lengths, on the GPU, the pages they take or give back, and the
+ * places of the step's rows. With n = new_tokens[r] and len = kv_len[r] of request r:
+ *   n >= 0  the request gets rows for tokens len .. len+n-1 (n = 0: none; a decoding request: 1; a
+ *           prompt: its length). Its page table entries 0 .. ceil(len/page_tokens)-1 are in place;
+ *           the entries up to ceil((len+n)/page_tokens)-1 are popped off the free ring, requests in
+ *           order. kv_len_out[r] = len + n.
+ *   n = -1  the request leaves: its ceil(len/page_tokens) pages are pushed onto the ring, requests
+ *           in order, for later calls (this call's new entries come from the pages that were free
+ *           before it). kv_len_out[r] = 0; its page table row is left as it is.
+ * The ring is free_ring[num_pages] with free_state = {head, count}: the free pages are entries
+ * head, head+1, .. head+count-1 (mod num_pages); pops move the head, pushes go behind the last.
+ * Rows follow in request order, then padding up to num_rows:
+ *   row_request[i], position[i] (the token's index in its request), cache_slot[i] (page *
+ *   page_tokens + position % page_tokens), row_slot[i] (the request's adapter): -1 in padding;
+ *   seg_offsets[num_requests+2], seg_slot[num_requests+1]: the rows as SGMV segments, one per
+ *   request with its adapter slot and a last one for the padding with slot -1.
+ * Sums are over whole numbers and every place is determined by the inputs.
+ * Errors, in which case the call changes no page and no length (kv_len_out = kv_len,
+ * free_state_out = free_state) and lays every row out as padding:
+ *   NO_PAGES    the ring holds fewer pages than the requests need
+ *   BAD_LENGTH  kv_len[r] < 0, n < -1, len + n > max_pages * page_tokens, more than num_rows rows,
+ *               head outside [0, num_pages), count outside [0, num_pages] or pushed beyond num_pages
+ *   BAD_PAGE    (only this row) the row's page id is outside [0, num_pages): its cache_slot is -1 */
+typedef struct {
+  int32_t num_requests;        /* 0 .. MLORA_KV_MAX_REQUESTS */
+  int32_t num_rows;            /* entries of the row arrays */
+  int32_t page_tokens;         /* tokens of a page */
+  int32_t max_pages;           /* entries of a page table row; max_pages * page_tokens < 2^31 */
+  int32_t num_pages;           /* entries of free_ring; page ids are 0 .. num_pages-1 */
+  int64_t table_stride;        /* page table: int32 from one request's row to the next, >= max_pages */
+  const int32_t *new_tokens;   /* [num_requests] */
+  const int32_t *kv_len;       /* [num_requests] tokens in the cache before this step */
+  int32_t *kv_len_out;         /* [num_requests] tokens after it; may be kv_len */
+  int32_t *page_table;         /* [num_requests][table_stride], in and out */
+  int32_t *free_ring;          /* [num_pages], in and out */
+  const int32_t *free_state;   /* [2] head, count */
+  int32_t *free_state_out;     /* [2]; may be free_state */
+  const int32_t *adapter_slot; /* [num_requests], or NULL: every adapter slot written is -1 */
+  int32_t *row_request;        /* [num_rows] */
+  int32_t *position;           /* [num_rows] */
+  int64_t *cache_slot;         /* [num_rows] */
+  int32_t *row_slot;           /* [num_rows], or NULL */
+  int32_t *seg_offsets;        /* [num_requests + 2], or NULL */
+  int32_t *seg_slot;           /* [num_requests + 1], or NULL */
+} mlora_kv_batch;
+
+MLORA_API int lora_kv_layout(const mlora_kv_batch *batch, int32_t *dev_status, void *stream);
+
+/* A paged key-value cache. Element d of token t of head h in page p of a layer is at
+ *   k + p * page_stride + layer * layer_stride + t * token_stride + h * head_stride + d
+ * and v likewise (strides in elements, multiples of 8; k and v 16-byte aligned). Token j of request r
+ * is token j % page_tokens of page page_table[r][j / page_tokens]. */
+typedef struct {
+  int32_t dtype;        /* MLORA_BF16 or MLORA_FP16: the type of the cache, q, k, v and the output */
+  int32_t num_layers;
+  int32_t num_kv_heads;
+  int32_t head_dim;     /* a multiple of 8, 8 .. MLORA_KV_MAX_HEAD_DIM */
+  int32_t page_tokens;
+  int32_t num_pages;
+  void *k, *v;
+  int64_t page_stride, layer_stride, token_stride, head_stride;
+} mlora_kv_cache;
+
+/* lora_kv_append: for every row i with cache_slot[i] >= 0, store its k and v heads in the cache, k
+ * rotated by the row's position, and its q heads, rotated likewise, in q_out (no q: q = NULL, num_q_heads
+ * = 0). Rotary positions: with c, s = rope_cos, rope_sin[position[i]][m], 0 <= m < rotary_dim / 2,
+ *   (a, b) -> (a c - b s, b c + a s),  in fp32, rounded once to the cache's type, for
+ *   (a, b) = elements (m, m + rotary_dim/2) of a head, or (2m, 2m+1) with rope_interleaved;
+ * the elements from rotary_dim on, and all of them without tables (rope_cos = NULL), are copied.
+ * Two rows with the same cache slot leave either's values there. q_out may be q. Rows are
+ * ldk, ldv, ldq, ldq_out elements apart (multiples of 8; pointers 16-byte aligned).
+ * Skipped rows, with their status: a slot < -1 or >= num_pages * page_tokens (BAD_SLOT), a position
+ * outside [0, max_position) where there are tables (BAD_LENGTH). */
+typedef struct {
+  int32_t num_rows, num_q_heads;
+  const int64_t *cache_slot; /* [num_rows] */
+  const int32_t *position;   /* [num_rows]; NULL without tables */
+  const void *k, *v, *q;     /* [num_rows][ldk >= num_kv_heads * head_dim], .. */
+  void *q_out;
+  int64_t ldk, ldv, ldq, ldq_out;
+  const float *rope_cos, *rope_sin; /* [max_position][rotary_dim / 2] fp32, contiguous, 16-byte aligned, or both NULL */
+  int32_t rotary_dim;        /* a multiple of 16, at most head_dim; 0 without tables */
+  int32_t max_position, rope_interleaved;
+} mlora_kv_rows;
+
+MLORA_API int lora_kv_append(const mlora_kv_cache *cache, const mlora_kv_rows *rows, int32_t layer,
+                             int32_t *dev_status, void *stream);
+
+/* lora_kv_attention: for every row i and query head h, over the tokens t of its request
+ * row_request[i] that it sees, max(0, position[i] + 1 - window) <= t <= position[i] (window = 0: from
+ * token 0),
+ *   w_t = exp(scale q[i][h] . K[t][h / G]) / sum of these,   out[i][h] = sum_t w_t V[t][h / G],
+ *   lse[i][h] = log of that sum,   G = num_q_heads / num_kv_heads,
+ * the scores, the sums and the softmax's statistics in fp32, the output rounded once. A row with
+ * position -1 sees nothing: its output is 0 and its lse -inf. Several rows of one request (a drafted
+ * continuation, the rows of a prompt) are rows of their own. Cache contents outside the tokens that a
+ * row sees, NaN included, do not reach its output. The long rows' tokens are split over the whole GPU
+ * and joined in a fixed order: the same call gives the same bits.
+ * workspace: lora_kv_attention_workspace bytes of device memory, 16-byte aligned, zeroed by the
+ * caller before its first use; every call leaves the part that has to be zero at zero. Calls that may
+ * run at the same time need workspaces of their own.
+ * Status: a row_request outside [0, num_requests) (BAD_REQUEST) or a position outside [-1, max_pages *
+ * page_tokens) (BAD_LENGTH): the row's output and lse are left untouched. A page id outside [0, num_pages)
+ * (BAD_PAGE): the page's tokens count as not seen. */
+typedef struct {
+  int32_t num_rows, num_q_heads; /* num_q_heads a multiple of the cache's num_kv_heads */
+  const void *q;                 /* [num_rows][ldq >= num_q_heads * head_dim] */
+  void *out;                     /* [num_rows][ldo] */
+  int64_t ldq, ldo;              /* multiples of 8 */
+  const int32_t *position;       /* [num_rows] */
+  const int32_t *row_request;    /* [num_rows], or NULL: row i is request i */
+  const int32_t *page_table;     /* [num_requests][table_stride] */
+  int64_t table_stride;
+  int32_t num_requests, max_pages; /* max_pages * page_tokens < 2^31 */
+  int32_t window;
+  float scale;
+  float *lse;                    /* [num_rows][num_q_heads], or NULL */
+  void *workspace;
+  int64_t workspace_bytes;
+} mlora_kv_attn;
+
+/* Bytes of workspace that lora_kv_attention needs on this cache, whatever the batch. */
+MLORA_API int64_t lora_kv_attention_workspace(const mlora_kv_cache *cache, int32_t num_q_heads);
+MLORA_API int lora_kv_attention(const mlora_kv_cache *cache, const mlora_kv_attn *args, int32_t layer,
+                                int32_t *dev_status, void *stream);
+
+/* lora_logits_adjust: out[i][t] from logits[i][t], for row i of request r = row_request[i] (-1: the row's
+ * output is left untouched), in fp32 and rounded once to the logits' type. With the request's history
+ * tokens[r][0 .. total_len[r]), of which the first prompt_len[r] are its prompt,
+ *   x = logits[i][t]
+ *   t in the history:              x = x > 0 ? x / repetition[r] : x * repetition[r]
+ *   t c > 0 times past the prompt: x = x - frequency[r] * c - presence[r]
+ *   t in the request's bias list:  x = x + its value (of several entries with one id, the last)
+ *   temperature[r] > 0:            x = x / temperature[r]
+ *   mask_index[r] >= 0 and bit t % 32 of mask[mask_index[r]][t / 32] is 0: x = -inf
+ * Every array may be NULL and then has no part (tokens, prompt_len and total_len together; bias_offsets,
+ * bias_token and bias_value; mask and mask_index). logits and out are rows ld, ldo elements apart, aligned
+ * to their element; out may be logits.
+ * Status: a token id outside [0, vocab) in a history or a bias list (BAD_TOKEN): that entry has no
+ * part. total_len[r] outside [0, tokens_stride] or prompt_len[r] outside [0, total_len[r]] or bias offsets
+ * that decrease or leave [0, num_bias] (BAD_LENGTH), mask_index[r] outside [-1, num_masks) (BAD_SLOT), row_request[i]
+ * outside [-1, num_requests) (BAD_REQUEST): the row is skipped. */
+typedef struct {
+  int32_t num_rows, vocab, dtype; /* dtype: MLORA_FP32, MLORA_BF16 or MLORA_FP16 */
+  int32_t num_requests;
+  const void *logits;
+  void *out;
+  int64_t ld, ldo;
+  const int32_t *row_request;     /* [num_rows], or NULL: row i is request i */
+  const int32_t *tokens;          /* [num_requests][tokens_stride] */
+  int64_t tokens_stride;
+  const int32_t *prompt_len, *total_len;                        /* [num_requests] */
+  const float *repetition, *presence, *frequency, *temperature; /* [num_requests] each */
+  const int32_t *bias_offsets;    /* [num_requests + 1] */
+  const int32_t *bias_token;
+  const float *bias_value;
+  int32_t num_bias;               /* entries of bias_token and bias_value */
+  const uint32_t *mask;           /* [num_masks][mask_stride >= ceil(vocab / 32)] */
+  int64_t mask_stride;
+  const int32_t *mask_index;      /* [num_requests] */
+  int32_t num_masks;
+} mlora_logits;
+
+MLORA_API int lora_logits_adjust(const mlora_logits *args, int32_t *dev_status, void *stream);
 
 /* ---- utilities --------------------------------------------------------------------------- */
 

@@ -43,11 +43,10 @@ constexpr int kMaxGroup = 16;        // query heads of a work item
 constexpr float kSlack = 8.f;        // log2 of how far a weight may pass 1 before m moves
 
 constexpr int attn_warps(int dp) { return dp == 256 ? 4 : 8; }
-constexpr int attn_stages(int dp) { return dp == 64 ? 6 : 3; }
+constexpr int attn_stages(int dp) { return dp == 64 ? 4 : 2; }
 // Floats of a partial result: out [16][dp], then m [16] and l [16].
 constexpr int partial_floats(int dp) { return kMaxGroup * (dp + 2); }
-// Partial results of a CTA in the workspace: one a warp, two of its own.
-constexpr int partial_slots(int dp) { return attn_warps(dp) + 2; }
+constexpr int kPartialSlots = 2;  // partial results of a CTA in the workspace
 constexpr int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 struct AttnParams {
@@ -59,8 +58,13 @@ struct AttnParams {
   int32_t group, chunks;  // query heads of a key-value head, in chunks of at most 16
   float scale_log2;       // scale * log2(e)
   int32_t *counters;      // [CTAs], zero between calls
-  float *partials;        // [CTAs][partial_slots][partial_floats]
+  float *partials;        // [CTAs][kPartialSlots][partial_floats]
 };
+
+// a / b for a >= 0, b > 0
+__device__ __forceinline__ int64_t quick_div(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 32) ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {  // ex2.approx: 2 ulp, exact limits
   float y;
@@ -109,6 +113,9 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint3
 }
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async4(void *dst_smem, const void *src_gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst_smem)), "l"(src_gmem) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -123,20 +130,30 @@ struct Tile {
 };
 constexpr uint32_t kFirst = 1u << 30, kLast = 1u << 31, kRowMask = kFirst - 1;
 
-template <int DP, int NW>
+template <int DP, int NW, int NB>
 struct AttnSmem {
   static constexpr int kStages = attn_stages(DP);
   static constexpr int kStageElems = 2 * kTile * DP;  // K, then V
-  // a warp's tiles; after its last tile, its two unfinished pieces [2][16][DP] fp32
-  uint16_t ring[NW][kStages][kStageElems];
-  int64_t first[kRowsPerLaunch + 1];  // tiles (of one head) before a row
-  int32_t pos[kRowsPerLaunch];        // last token seen; -1: none, -2: a bad row
-  uint32_t seen[NW][kStages];         // bit t: token t of the tile is seen
+  uint16_t ring[NW][kStages][kStageElems];  // a warp's tiles; after the last, its unfinished last piece
+  float head[NW][NB * 8][DP];               // its unfinished first piece
+  int64_t first[kRowsPerLaunch + 1];        // tiles (of one head) before a row
+  int32_t pos[kRowsPerLaunch];              // last token seen; -1: none, -2: a bad row
+  int32_t req[kRowsPerLaunch];              // the row's request
+  uint32_t seen[NW][kStages];               // bit t: token t of the tile is seen
   int64_t warp_sum[NW];
-  float m[2 * NW][kMaxGroup], l[2 * NW][kMaxGroup];  // of the pieces: [2w] without the first tile, [2w+1] with it
+  int32_t page_id[NW][2 * kStages][kTile];  // pages of tokens, where a page does not hold whole tiles
+  // pieces: [2w] without the first tile of its (row, head), [2w+1] with it
+  float m[2 * NW][kMaxGroup], l[2 * NW][kMaxGroup];  // m, l; when joined, the piece's weight in m
   int32_t piece_row[2 * NW], piece_hc[2 * NW];
-  int32_t run[2 * NW + 1], runs;  // where the joined pieces of one (row, head) start, in order[]
-  int32_t order[2 * NW];
+  int32_t order[2 * NW];  // the pieces in the order of the list
+  struct Run {            // those of one (row, head)
+    int64_t out;          // place in out, or in partials (a run this CTA shares)
+    int32_t from, to;     // in order[]
+    int32_t row, hc, heads;
+    int32_t done, here;
+  } run[2 * NW];
+  float top[kMaxGroup], sum[kMaxGroup];
+  int32_t runs;
   int32_t last[2];
 };
 
@@ -145,11 +162,11 @@ template <int DT, int DP, int NB, bool PAGED16>
 __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     kv_attention_kernel(const __grid_constant__ AttnParams p, int32_t *status) {
   constexpr int NW = attn_warps(DP), NT = NW * 32;
-  using Smem = AttnSmem<DP, NW>;
+  using Smem = AttnSmem<DP, NW, NB>;
   constexpr int S = Smem::kStages;
   constexpr int CH = DP / 8;    // 16-byte chunks of a token's head
   constexpr int GP = NB * 8;    // heads that a piece holds
-  static_assert(2 * GP * DP * 4 <= S * Smem::kStageElems * 2, "the pieces fit in the ring");
+  static_assert(GP * DP * 4 <= S * Smem::kStageElems * 2, "a piece fits in the ring");
   // fp16 weights: up to 2^15 (with kSlack), so that small ones stay out of fp16's subnormals
   constexpr float kShift = DT == MLORA_FP16 ? 7.f : 0.f;
   extern __shared__ __align__(128) char smem_raw[];
@@ -178,6 +195,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         n = pos / kTile - lo / kTile + 1;
       }
       sh.pos[r] = pos;
+      sh.req[r] = req;
       sh.first[r] = n;
       sum += n;
     }
@@ -214,22 +232,37 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
   }
 
   // ---- this CTA's and this warp's part of it -----------------------------------------------------
+  // Even shares: the first `rest` CTAs (warps) take a tile more.
   const int64_t T = sh.first[R] * HC;
   const int64_t shares = (T + kMinTiles - 1) / kMinTiles;
   const int C = (int)min((int64_t)gridDim.x, shares);
   if ((int)blockIdx.x >= C) return;
-  const int nw = (int)min((int64_t)NW, (shares + C - 1) / C);
-  const int64_t t0 = blockIdx.x * T / C, t1 = (blockIdx.x + 1) * T / C;
-  const int64_t w0 = t0 + warp * (t1 - t0) / nw, w1 = warp < nw ? t0 + (warp + 1) * (t1 - t0) / nw : w0;
+  const int64_t share = quick_div(T, C), rest = T - share * C;
+  auto first_of = [&](int64_t cta) { return cta * share + min(cta, rest); };
+  auto cta_of = [&](int64_t tile) {
+    return (int)(tile < rest * (share + 1) ? quick_div(tile, share + 1) : rest + quick_div(tile - rest * (share + 1), share));
+  };
+  const int64_t t0 = first_of(blockIdx.x), t1 = first_of(blockIdx.x + 1);
+  const int nw = shares >= (int64_t)C * NW ? NW : (int)((shares + C - 1) / C);
+  const int64_t each = nw == NW ? (t1 - t0) / NW : quick_div(t1 - t0, nw), over = t1 - t0 - each * nw;
+  const int64_t w0 = t0 + warp * each + min((int64_t)warp, over);
+  const int64_t w1 = warp < nw ? w0 + each + (warp < over ? 1 : 0) : w0;
   const int n = (int)(w1 - w0);
 
-  float *const partials = p.partials + (int64_t)blockIdx.x * partial_slots(DP) * partial_floats(DP);
+  // the query heads of an item: the first one's number, and how many
+  auto heads_of = [&](int hc, int64_t &head0) {
+    const int hk = p.chunks == 1 ? hc : hc / p.chunks, g0 = p.chunks == 1 ? 0 : (hc - hk * p.chunks) * kMaxGroup;
+    head0 = (int64_t)hk * p.group + g0;
+    return min(p.group - g0, kMaxGroup);
+  };
+  float *const partials = p.partials + (int64_t)blockIdx.x * kPartialSlots * partial_floats(DP);
   // chunks past the head's end are never copied: zero for good
   if (D < DP) {
     for (int i = lane; i < S * Smem::kStageElems / 8; i += 32)
       reinterpret_cast<uint4 *>(sh.ring[warp])[i] = make_uint4(0, 0, 0, 0);
     __syncwarp();
   }
+  int pieces = 0;
   if (n > 0) {
     // tiles w0 + 32 b + lane
     auto place = [&](int b) {
@@ -244,7 +277,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       }
       const int nt = (int)(sh.first[r + 1] - sh.first[r]);
       const int64_t rem = x - sh.first[r] * HC;
-      t.hc = rem < nt ? 0 : (int)(rem / nt);
+      t.hc = rem < nt ? 0 : (int)quick_div(rem, nt);
       const int tile = (int)(rem - (int64_t)t.hc * nt);
       const int pos = sh.pos[r], lo = a.window ? max(0, pos + 1 - a.window) : 0;
       const int t0 = (lo / kTile + tile) * kTile;
@@ -253,7 +286,12 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       if (pos - t0 < kTile - 1) t.seen &= (2u << (pos - t0)) - 1u;
       t.row = (uint32_t)r | (tile == 0 ? kFirst : 0u) | (tile == nt - 1 ? kLast : 0u);
       const int64_t row = (int64_t)p.row0 + r;
-      const int req = a.row_request ? a.row_request[row] : (int)row;
+      const int req = sh.req[r];
+      if (tile == 0 || x == w0) {  // q of the (row, head), into L2
+        int64_t head0;
+        const int heads = heads_of(t.hc, head0);
+        prefetch_l2(static_cast<const uint16_t *>(a.q) + row * a.ldq + head0 * D, (uint32_t)(heads * D * 2));
+      }
       if constexpr (PAGED16) {
         const int pg = div_by(p.page, t0);
         const int id = a.page_table[(int64_t)req * a.table_stride + pg];
@@ -272,28 +310,26 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     Tile cur = place(0), nxt{};
     if (n > 32) nxt = place(1);
     int cur_batch = 0;
+    auto tile_at = [&](int i) -> const Tile & { return (i >> 5) == cur_batch ? cur : nxt; };
 
     // ---- loads, S - 1 tiles ahead of the products --------------------------------------------------
     const int lt = lane / CH, lc = lane % CH;  // a lane's token and chunk within a step of 32 chunks
     constexpr int kStep = 32 / CH;             // tokens of such a step
     const bool mine = lc * 8 < D;
-    // pages of other sizes: each token's page, looked up a tile before its copies start
-    int id = -1, inpage = 0, kv_head = 0;
-    uint32_t range = 0;
+    // Pages of other sizes: the page of each token of a tile, copied to shared memory S tiles before
+    // the tile's own copies start (with the copies of a tile that is waited for before that).
     auto look_up = [&](int i) {
-      const Tile &b = (i >> 5) == cur_batch ? cur : nxt;
+      const Tile &b = tile_at(i);
       const int64_t at = __shfl_sync(~0u, b.off, i & 31);
-      const int hc = __shfl_sync(~0u, b.hc, i & 31);
-      range = __shfl_sync(~0u, b.seen, i & 31);
-      const int t = (int)(uint32_t)at + (lane & 15), pg = div_by(p.page, t);
-      inpage = t - pg * p.page.d;
-      id = (range >> (lane & 15)) & 1u ? a.page_table[(at >> 32) * a.table_stride + pg] : -1;
-      kv_head = p.chunks == 1 ? hc : hc / p.chunks;
+      const uint32_t range = __shfl_sync(~0u, b.seen, i & 31);
+      const int t = (int)(uint32_t)at + lane;
+      if (lane < kTile && ((range >> lane) & 1u))
+        cp_async4(&sh.page_id[warp][i % (2 * S)][lane], a.page_table + (at >> 32) * a.table_stride + div_by(p.page, t));
     };
     auto issue = [&](int i, int slot) {  // tile i into ring slot `slot`
       uint16_t *ks = sh.ring[warp][slot];
       if constexpr (PAGED16) {
-        const Tile &b = (i >> 5) == cur_batch ? cur : nxt;
+        const Tile &b = tile_at(i);
         const int64_t off = __shfl_sync(~0u, b.off, i & 31);
         const uint32_t seen = __shfl_sync(~0u, b.seen, i & 31);
         if (lane == 0) sh.seen[warp][slot] = seen;
@@ -312,10 +348,16 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
           }
         }
       } else {
-        const bool want = (range >> (lane & 15)) & 1u, good = want && id >= 0 && id < p.c.num_pages;
+        const Tile &b = tile_at(i);
+        const int hc = __shfl_sync(~0u, b.hc, i & 31);
+        const int t0 = (int)(uint32_t)__shfl_sync(~0u, b.off, i & 31) + (lane & 15);
+        const bool want = (__shfl_sync(~0u, b.seen, i & 31) >> (lane & 15)) & 1u;
+        const int id = want ? sh.page_id[warp][i % (2 * S)][lane & 15] : -1;
+        const bool good = id >= 0 && id < p.c.num_pages;
         if (want && !good) report(status, MLORA_STATUS_BAD_PAGE);
-        const int64_t off = good ? (int64_t)id * p.c.page_stride + (int64_t)inpage * p.c.token_stride +
-                                       (int64_t)kv_head * p.c.head_stride
+        const int64_t off = good ? (int64_t)id * p.c.page_stride +
+                                       (int64_t)(t0 - div_by(p.page, t0) * p.page.d) * p.c.token_stride +
+                                       (int64_t)(p.chunks == 1 ? hc : hc / p.chunks) * p.c.head_stride
                                  : 0;
         const uint32_t seen = __ballot_sync(~0u, good) & 0xFFFFu;
         if (lane == 0) sh.seen[warp][slot] = seen;
@@ -330,10 +372,15 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
             tc::cp_async16(dst + kTile * DP, p.v + (bytes ? o : 0), bytes);
           }
         }
-        if (i + 1 < n) look_up(i + 1);
+        if (i + S < n) look_up(i + S);
       }
     };
-    if constexpr (!PAGED16) look_up(0);
+    if constexpr (!PAGED16) {
+      for (int i = 0; i < min(S, n); ++i) look_up(i);
+      cp_async_commit();
+      cp_async_wait<0>();
+      __syncwarp();
+    }
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) {
       if (i < n) issue(i, i);
@@ -343,6 +390,26 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     // ---- products ----------------------------------------------------------------------------------
     const int g = lane >> 2, quad = lane & 3;
     uint32_t q[DP / 16][NB][2];  // Q^T: head elements kk * 16 + {0, 8} + quad * 2 + {0, 1}, head g of the block
+    uint32_t ahead[DP / 16][NB][2];  // the next (row, head)'s, on its way while the last tile before it is computed
+    auto load_q = [&](int i) {
+      const Tile &b = tile_at(i);
+      const int64_t r = (int64_t)p.row0 + (int)(__shfl_sync(~0u, b.row, i & 31) & kRowMask);
+      int64_t h0;
+      const int heads = heads_of(__shfl_sync(~0u, b.hc, i & 31), h0);
+      const uint16_t *qr = static_cast<const uint16_t *>(a.q) + r * a.ldq + h0 * D;
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int head = nb * 8 + g, d = kk * 16 + j * 8 + quad * 2;
+            ahead[kk][nb][j] =
+                head < heads && d < D ? *reinterpret_cast<const uint32_t *>(qr + (int64_t)head * D + d) : 0u;
+          }
+    };
+    constexpr bool kAhead = DP * NB < 512;  // (no registers left for it at 16 heads of 256)
+    if constexpr (kAhead) load_q(0);
     float o[DP / 16][NB][4];     // O^T: elements j * 16 + g (0, 1) and + 8 (2, 3), heads quad * 2 + {0, 1}
     float m[NB][2], l[NB][2];    // of heads quad * 2 + {0, 1}; l: of this lane's tokens
     bool start = true, with_first = false;
@@ -360,25 +427,16 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       }
       const uint32_t meta = __shfl_sync(~0u, cur.row, it & 31);
       if (start) {
+        if constexpr (!kAhead) load_q(it);
         row_in = (int)(meta & kRowMask);
         hc = __shfl_sync(~0u, cur.hc, it & 31);
         with_first = (meta & kFirst) != 0;
         row = (int64_t)p.row0 + row_in;
-        const int hk = p.chunks == 1 ? hc : hc / p.chunks;
-        const int g0 = p.chunks == 1 ? 0 : (hc - hk * p.chunks) * kMaxGroup;
-        gn = min(p.group - g0, kMaxGroup);
-        head0 = (int64_t)hk * p.group + g0;
-        const uint16_t *qr = static_cast<const uint16_t *>(a.q) + row * a.ldq + head0 * D;
+        gn = heads_of(hc, head0);
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int head = nb * 8 + g, d = kk * 16 + j * 8 + quad * 2;
-              q[kk][nb][j] =
-                  head < gn && d < D ? *reinterpret_cast<const uint32_t *>(qr + (int64_t)head * D + d) : 0u;
-            }
+          for (int nb = 0; nb < NB; ++nb) q[kk][nb][0] = ahead[kk][nb][0], q[kk][nb][1] = ahead[kk][nb][1];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -388,6 +446,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         }
         start = false;
       }
+      if (kAhead && (meta & kLast) && it + 1 < n) load_q(it + 1);  // the next tile begins another (row, head)
       if (it + S - 1 < n) issue(it + S - 1, slot == 0 ? S - 1 : slot - 1);
       cp_async_commit();
       cp_async_wait<S - 1>();
@@ -491,11 +550,10 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
                     l[nb][j] == 0.f ? -CUDART_INF_F : (m[nb][j] - kShift) * CUDART_LN2_F + logf(l[nb][j]);
             }
         } else {
-          // a piece: at the end of the warp's tiles into its (then idle) ring, before that to the workspace
+          // with the first tile it is the warp's last piece, and the ring is idle
           const int piece = 2 * warp + (with_first ? 1 : 0);
-          float *part = it == n - 1 ? reinterpret_cast<float *>(sh.ring[warp]) + (piece & 1) * GP * DP
-                                    : partials + warp * partial_floats(DP);
-          if (it == n - 1) {
+          float *part = with_first ? reinterpret_cast<float *>(sh.ring[warp]) : sh.head[warp][0];
+          if (with_first) {
             cp_async_wait<0>();
             __syncwarp();
           }
@@ -512,141 +570,195 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
               }
               if (g == 0) sh.m[piece][head] = m[nb][j], sh.l[piece][head] = l[nb][j];
             }
-          if (lane == 0) {
-            sh.piece_row[piece] = row_in;
-            sh.piece_hc[piece] = hc | (it == n - 1 ? 0 : 1 << 30);  // bit 30: in the workspace
-          }
+          if (lane == 0) sh.piece_row[piece] = row_in, sh.piece_hc[piece] = hc;
+          pieces = 1;
         }
       }
     }
-    // a piece that went to the workspace comes back beside the other
     cp_async_wait<0>();
-    __syncwarp();
-    if (sh.piece_row[2 * warp] >= 0 && (sh.piece_hc[2 * warp] >> 30)) {
-      const float *part = partials + warp * partial_floats(DP);
-      const int c = sh.piece_hc[2 * warp] & ~(1 << 30);
-      const int heads = min(p.group - (c % p.chunks) * kMaxGroup, kMaxGroup);
-      for (int i = lane; i < heads * DP / 4; i += 32)
-        reinterpret_cast<float4 *>(sh.ring[warp])[i] = __ldcg(reinterpret_cast<const float4 *>(part) + i);
-      __syncwarp();
-      if (lane == 0) sh.piece_hc[2 * warp] = c;
-    }
   }
-  __syncthreads();
+  if (!__syncthreads_or(pieces)) return;
 
   // ---- join the pieces of the CTA's warps, then those of the CTAs ------------------------------------
-  if (tid == 0) {  // runs of pieces of one (row, head), in the order of the list
-    int runs = 0, count = 0;
-    for (int e = 0; e < 2 * nw; ++e) {
-      if (sh.piece_row[e] < 0) continue;
-      const int before = count ? sh.order[count - 1] : -1;
-      if (before < 0 || sh.piece_row[before] != sh.piece_row[e] || sh.piece_hc[before] != sh.piece_hc[e])
-        sh.run[runs++] = count;
-      sh.order[count++] = e;
+  // Runs of pieces of one (row, head), in the order of the list: lane e looks at piece e. A run that began in
+  // an earlier CTA (the first) goes to the CTA's partial result 0, one that goes on in a later one (the
+  // last) to 1, the others to the output.
+  if (warp == 0) {
+    const int r = lane < 2 * nw ? sh.piece_row[lane] : -1, c = lane < 2 * nw ? sh.piece_hc[lane] : 0;
+    const uint32_t any = __ballot_sync(~0u, r >= 0);
+    const uint32_t below = any & ((1u << lane) - 1u);
+    const int before = below ? 31 - __clz(below) : 0;
+    const int r0 = __shfl_sync(~0u, r, before), c_before = __shfl_sync(~0u, c, before);
+    const bool starts = r >= 0 && (!below || r0 != r || c_before != c);
+    const uint32_t all = __ballot_sync(~0u, starts);
+    if (r >= 0) sh.order[__popc(below)] = lane;
+    if (starts) {
+      const uint32_t later = lane == 31 ? 0u : all >> (lane + 1);
+      const uint32_t until = later ? any & ((2u << (lane + __ffs(later) - 1)) - 1u) : any;
+      auto &run = sh.run[__popc(all & ((1u << lane) - 1u))];
+      run.from = __popc(below);
+      run.to = __popc(until);
+      run.row = r;
+      run.hc = c;
+      const int64_t nt = sh.first[r + 1] - sh.first[r], begin = sh.first[r] * HC + c * nt;
+      run.here = begin >= t0;
+      run.done = run.here && begin + nt <= t1;
+      int64_t head0;
+      run.heads = heads_of(c, head0);
+      run.out = run.done ? ((int64_t)p.row0 + r) * a.ldo + head0 * D : run.here * (int64_t)partial_floats(DP);
     }
-    sh.run[runs] = count;
-    sh.runs = runs;
+    if (lane == 0) sh.runs = __popc(all);
   }
   __syncthreads();
-  // The first run may have begun in an earlier CTA (it goes to the CTA's partial result 0), the last may go
-  // on in a later one (1).
-  int open_row[2] = {-1, -1}, open_hc[2] = {0, 0};
-  auto emit = [&](int64_t row, int64_t head, int d, float4 acc, float top, float sum) {
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (d < D) {
-      uint2 u;
-      u.x = (uint32_t)Elem<DT>::from_float(acc.x * inv) | ((uint32_t)Elem<DT>::from_float(acc.y * inv) << 16);
-      u.y = (uint32_t)Elem<DT>::from_float(acc.z * inv) | ((uint32_t)Elem<DT>::from_float(acc.w * inv) << 16);
-      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * a.ldo + head * D + d) = u;
+  const int runs = sh.runs;
+  auto lse_of = [&](float m, float l) { return l == 0.f ? -CUDART_INF_F : (m - kShift) * CUDART_LN2_F + logf(l); };
+  // a run's maximum and sum, and from them each piece's weight
+  for (int i = tid; i < runs * GP; i += NT) {
+    const auto &run = sh.run[i / GP];
+    const int head = i % GP;
+    if (head >= run.heads) continue;
+    float top = -CUDART_INF_F, sum = 0.f;
+    for (int k = run.from; k < run.to; ++k) top = fmaxf(top, sh.m[sh.order[k]][head]);
+    const float base = top == -CUDART_INF_F ? 0.f : top;
+    for (int k = run.from; k < run.to; ++k) {
+      const int e = sh.order[k];
+      sum += exp2_fast(sh.m[e][head] - base) * sh.l[e][head];
     }
-    if (a.lse && d == 0)
-      a.lse[row * a.num_q_heads + head] = sum == 0.f ? -CUDART_INF_F : (top - kShift) * CUDART_LN2_F + logf(sum);
+    const float inv = !run.done ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+    for (int k = run.from; k < run.to; ++k) {
+      const int e = sh.order[k];
+      sh.m[e][head] = exp2_fast(sh.m[e][head] - base) * inv;
+    }
+    if (run.done) {
+      int64_t head0;
+      heads_of(run.hc, head0);
+      if (a.lse) a.lse[((int64_t)p.row0 + run.row) * a.num_q_heads + head0 + head] = lse_of(top, sum);
+    } else {
+      float *to = partials + run.out + kMaxGroup * DP + head;
+      to[0] = top, to[16] = sum;
+    }
+  }
+  __syncthreads();
+  auto pack4 = [&](float4 f) {
+    uint2 u;
+    u.x = (uint32_t)Elem<DT>::from_float(f.x) | ((uint32_t)Elem<DT>::from_float(f.y) << 16);
+    u.y = (uint32_t)Elem<DT>::from_float(f.z) | ((uint32_t)Elem<DT>::from_float(f.w) << 16);
+    return u;
   };
   constexpr int kUnits = GP * (DP / 4);  // four elements of a head
-  const int runs = sh.runs;
-  for (int u = 0; u < runs; ++u) {
-    const int e0 = sh.order[sh.run[u]], r = sh.piece_row[e0], c = sh.piece_hc[e0];
-    const int64_t nt = sh.first[r + 1] - sh.first[r], begin = sh.first[r] * HC + c * nt;
-    const bool here = begin >= t0, done = here && begin + nt <= t1;
-    if (!done) open_row[here] = r, open_hc[here] = c;
-    const int hk = c / p.chunks, g0 = (c - hk * p.chunks) * kMaxGroup, heads = min(p.group - g0, kMaxGroup);
-    float *to = partials + (NW + (here ? 1 : 0)) * partial_floats(DP);
-    for (int i = tid; i < kUnits; i += NT) {
-      const int head = i / (DP / 4), d = (i % (DP / 4)) * 4;
-      if (head >= heads) break;
-      float top = -CUDART_INF_F, sum = 0.f;
-      for (int k = sh.run[u]; k < sh.run[u + 1]; ++k) top = fmaxf(top, sh.m[sh.order[k]][head]);
-      const float base = top == -CUDART_INF_F ? 0.f : top;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = sh.run[u]; k < sh.run[u + 1]; ++k) {
-        const int e = sh.order[k];
-        const float w = exp2_fast(sh.m[e][head] - base);
-        const float4 f = reinterpret_cast<const float4 *>(sh.ring[e >> 1])[(e & 1) * kUnits + i];
-        sum += w * sh.l[e][head];
-        acc.x += w * f.x, acc.y += w * f.y, acc.z += w * f.z, acc.w += w * f.w;
-      }
-      if (done) {
-        emit((int64_t)p.row0 + r, (int64_t)hk * p.group + g0 + head, d, acc, top, sum);
-      } else {
-        *reinterpret_cast<float4 *>(to + head * DP + d) = acc;
-        if (d == 0) to[kMaxGroup * DP + head] = top, to[kMaxGroup * DP + 16 + head] = sum;
-      }
+#pragma unroll 2
+  for (int x = tid; x < runs * kUnits; x += NT) {
+    const auto &run = sh.run[x / kUnits];
+    const int i = x % kUnits, head = i / (DP / 4), d = (i % (DP / 4)) * 4;
+    if (head >= run.heads) continue;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = run.from; k < run.to; ++k) {
+      const int e = sh.order[k];
+      const float w = sh.m[e][head];
+      const float4 f = (e & 1 ? reinterpret_cast<const float4 *>(sh.ring[e >> 1])
+                              : reinterpret_cast<const float4 *>(sh.head[e >> 1][0]))[i];
+      acc.x += w * f.x, acc.y += w * f.y, acc.z += w * f.z, acc.w += w * f.w;
+    }
+    if (run.done) {
+      if (d < D) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + run.out + head * D + d) = pack4(acc);
+    } else {
+      *reinterpret_cast<float4 *>(partials + run.out + head * DP + d) = acc;
     }
   }
-  if (open_row[0] < 0 && open_row[1] < 0) return;
-  __threadfence();
+  // The items this CTA shares with others: the run that began before it, and the one that goes on behind it.
+  int open[2] = {-1, -1};
+  if (runs && !sh.run[0].here) open[0] = 0;
+  if (runs && sh.run[runs - 1].here && !sh.run[runs - 1].done) open[1] = runs - 1;
+  if (open[0] < 0 && open[1] < 0) return;
   __syncthreads();
-  int64_t c0[2], c1[2];  // first and last CTA of the open items
+  int c0[2], c1[2];  // first and last CTA of such an item
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if (open_row[h] < 0) continue;
-    const int64_t nt = sh.first[open_row[h] + 1] - sh.first[open_row[h]];
-    const int64_t begin = sh.first[open_row[h]] * HC + open_hc[h] * nt;
-    c0[h] = ((begin + 1) * C - 1) / T;
-    c1[h] = ((begin + nt) * C - 1) / T;
-    if (tid == 0) {
-      const int before = atomicAdd(p.counters + c0[h], 1);
-      sh.last[h] = before == (int)(c1[h] - c0[h]);
-      if (sh.last[h]) p.counters[c0[h]] = 0;  // nobody else comes: back to zero for the next call
-    }
+    if (open[h] < 0) continue;
+    const int r = sh.run[open[h]].row;
+    const int64_t nt = sh.first[r + 1] - sh.first[r], begin = sh.first[r] * HC + sh.run[open[h]].hc * nt;
+    c0[h] = cta_of(begin);
+    c1[h] = cta_of(begin + nt - 1);
   }
-  if (tid == 0) __threadfence();
+  if (tid == 0) {
+    __threadfence();  // the CTA's partial results (seen here by the barrier) before the count
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (open[h] >= 0) {
+        const int before = atomicAdd(p.counters + c0[h], 1);
+        sh.last[h] = before == c1[h] - c0[h];
+        if (sh.last[h]) p.counters[c0[h]] = 0;  // nobody else comes: back to zero for the next call
+      }
+    __threadfence();
+  }
   __syncthreads();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if (open_row[h] < 0 || !sh.last[h]) continue;
-    const int count = (int)(c1[h] - c0[h] + 1), c = open_hc[h];
-    const int hk = c / p.chunks, g0 = (c - hk * p.chunks) * kMaxGroup, heads = min(p.group - g0, kMaxGroup);
+    if (open[h] < 0 || !sh.last[h]) continue;
+    const auto &run = sh.run[open[h]];
+    const int count = c1[h] - c0[h] + 1;
     auto at = [&](int k) {
-      return p.partials + ((c0[h] + k) * partial_slots(DP) + NW + (k == 0 ? 1 : 0)) * partial_floats(DP);
+      return p.partials + ((int64_t)(c0[h] + k) * kPartialSlots + (k == 0 ? 1 : 0)) * partial_floats(DP);
     };
+    float4 early[4] = {};  // few partial results: all on their way at once
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < count && tid < kUnits && tid / (DP / 4) < run.heads)
+        early[k] = __ldcg(reinterpret_cast<const float4 *>(at(k)) + tid);
+    float *w = reinterpret_cast<float *>(sh.ring[0]), *l = w + count * GP;  // [count][GP], in the idle ring
+    for (int i = tid; i < count * GP; i += NT) {
+      const float *x = at(i / GP) + kMaxGroup * DP + i % GP;
+      w[i] = __ldcg(x);
+      l[i] = __ldcg(x + 16);
+    }
+    __syncthreads();
+    if (tid < GP) {
+      float top = -CUDART_INF_F, sum = 0.f;
+      for (int k = 0; k < count; ++k) top = fmaxf(top, w[k * GP + tid]);
+      const float base = top == -CUDART_INF_F ? 0.f : top;
+      for (int k = 0; k < count; ++k) {
+        const float f = exp2_fast(w[k * GP + tid] - base);
+        sum += f * l[k * GP + tid];
+        w[k * GP + tid] = f;
+      }
+      sh.top[tid] = top;
+      sh.sum[tid] = sum;
+    }
+    __syncthreads();
+    int64_t head0;
+    heads_of(run.hc, head0);
+    const int64_t row = (int64_t)p.row0 + run.row;
     for (int i = tid; i < kUnits; i += NT) {
       const int head = i / (DP / 4), d = (i % (DP / 4)) * 4;
-      if (head >= heads) break;
-      float top = -CUDART_INF_F, sum = 0.f;
-#pragma unroll 8
-      for (int k = 0; k < count; ++k) top = fmaxf(top, __ldcg(at(k) + kMaxGroup * DP + head));
-      const float base = top == -CUDART_INF_F ? 0.f : top;
+      if (head >= run.heads) break;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](float x, const float4 &f) {
+        acc.x += x * f.x, acc.y += x * f.y, acc.z += x * f.z, acc.w += x * f.w;
+      };
+      int k = 0;
+      if (i == tid)
+#pragma unroll
+        for (; k < 4; ++k)
+          if (k < count) add(w[k * GP + head], early[k]);
 #pragma unroll 8
-      for (int k = 0; k < count; ++k) {
-        const float *x = at(k);
-        const float4 f = __ldcg(reinterpret_cast<const float4 *>(x + head * DP + d));
-        const float w = exp2_fast(__ldcg(x + kMaxGroup * DP + head) - base);
-        sum += w * __ldcg(x + kMaxGroup * DP + 16 + head);
-        acc.x += w * f.x, acc.y += w * f.y, acc.z += w * f.z, acc.w += w * f.w;
-      }
-      emit((int64_t)p.row0 + open_row[h], (int64_t)hk * p.group + g0 + head, d, acc, top, sum);
+      for (; k < count; ++k) add(w[k * GP + head], __ldcg(reinterpret_cast<const float4 *>(at(k)) + i));
+      const float inv = sh.sum[head] == 0.f ? 0.f : 1.f / sh.sum[head];
+      acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+      if (d < D)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * a.ldo + (head0 + head) * D + d) = pack4(acc);
+      if (a.lse && d == 0) a.lse[row * a.num_q_heads + head0 + head] = lse_of(sh.top[head], sh.sum[head]);
     }
+    __syncthreads();  // the other item uses the same places
   }
 }
 
-int attn_ctas() { return sm_count(); }
+// One per SM; at most as many as the weights of their partial results fit in a warp's ring.
+int attn_ctas() { return min(sm_count(), 192); }
 constexpr size_t kCounterBytes = 4096;  // more than any GPU's SMs
 
 template <int DT, int DP, int NB, bool PAGED16>
 cudaError_t launch(const AttnParams &p, int32_t *status, cudaStream_t stream) {
-  using Smem = AttnSmem<DP, attn_warps(DP)>;
+  using Smem = AttnSmem<DP, attn_warps(DP), NB>;
   static_assert(sizeof(Smem) <= 227 * 1024, "fits in shared memory");
   cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<DT, DP, NB, PAGED16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)sizeof(Smem));
@@ -676,7 +788,7 @@ cudaError_t dispatch(const AttnParams &p, int32_t *status, cudaStream_t stream) 
 
 int64_t kv_attention_workspace_bytes(int32_t head_dim) {
   const int dp = padded_dim(head_dim);
-  return (int64_t)kCounterBytes + (int64_t)attn_ctas() * partial_slots(dp) * partial_floats(dp) * sizeof(float);
+  return (int64_t)kCounterBytes + (int64_t)attn_ctas() * kPartialSlots * partial_floats(dp) * sizeof(float);
 }
 
 cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a, int32_t layer, int32_t *status,

@@ -38,7 +38,10 @@ namespace {
 
 constexpr int kTile = 16;            // tokens of a tile
 constexpr int kRowsPerLaunch = 1024;
-constexpr int kMinTiles = 4;         // a warp's share of a small call, so that few pieces have to be joined
+constexpr int kMinTiles = 2;         // a warp's share of a small call, so that few pieces have to be joined
+// A CTA's boundary inside a (row, head) of at most this many tiles moves to its nearer end, where the CTAs'
+// shares are at most kSmallShare tiles (above).
+constexpr int kSmallShare = 64, kWhole = 96, kWholeLarge = 24;
 constexpr int kMaxGroup = 16;        // query heads of a work item
 constexpr float kSlack = 8.f;        // log2 of how far a weight may pass 1 before m moves
 
@@ -143,17 +146,8 @@ struct AttnSmem {
   int64_t warp_sum[NW];
   int32_t page_id[NW][2 * kStages][kTile];  // pages of tokens, where a page does not hold whole tiles
   // pieces: [2w] without the first tile of its (row, head), [2w+1] with it
-  float m[2 * NW][kMaxGroup], l[2 * NW][kMaxGroup];  // m, l; when joined, the piece's weight in m
+  float m[2 * NW][kMaxGroup], l[2 * NW][kMaxGroup];
   int32_t piece_row[2 * NW], piece_hc[2 * NW];
-  int32_t order[2 * NW];  // the pieces in the order of the list
-  struct Run {            // those of one (row, head)
-    int64_t out;          // place in out, or in partials (a run this CTA shares)
-    int32_t from, to;     // in order[]
-    int32_t row, hc, heads;
-    int32_t done, here;
-  } run[2 * NW];
-  float top[kMaxGroup], sum[kMaxGroup];
-  int32_t runs;
   int32_t last[2];
 };
 
@@ -242,9 +236,33 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
   auto cta_of = [&](int64_t tile) {
     return (int)(tile < rest * (share + 1) ? quick_div(tile, share + 1) : rest + quick_div(tile - rest * (share + 1), share));
   };
-  const int64_t t0 = first_of(blockIdx.x), t1 = first_of(blockIdx.x + 1);
-  const int nw = shares >= (int64_t)C * NW ? NW : (int)((shares + C - 1) / C);
-  const int64_t each = nw == NW ? (t1 - t0) / NW : quick_div(t1 - t0, nw), over = t1 - t0 - each * nw;
+  // the last row with first[row] HC <= x, for x < T
+  auto row_of = [&](int64_t x) {
+    int r = 0;
+    for (int hi = R; hi - r > 1;) {
+      const int mid = (r + hi) >> 1;
+      if (sh.first[mid] * HC <= x) r = mid;
+      else hi = mid;
+    }
+    return r;
+  };
+  int64_t t0, t1;
+  {
+    int64_t x = first_of(blockIdx.x + (lane & 1));  // lanes 0 and 1: the CTA's two boundaries
+    if (x < T) {
+      const int r = row_of(x);
+      const int nt = (int)(sh.first[r + 1] - sh.first[r]);
+      if (nt <= (share <= kSmallShare ? kWhole : kWholeLarge)) {
+        const int64_t rem = x - sh.first[r] * HC;
+        const int in = (int)(rem - quick_div(rem, nt) * nt);
+        x += 2 * in < nt ? -in : nt - in;
+      }
+    }
+    t0 = __shfl_sync(~0u, x, 0), t1 = __shfl_sync(~0u, x, 1);
+  }
+  const int64_t mine = t1 - t0;
+  const int nw = mine >= (int64_t)NW * kMinTiles ? NW : max(1, (int)(mine + kMinTiles - 1) / kMinTiles);
+  const int64_t each = nw == NW ? mine / NW : quick_div(mine, nw), over = mine - each * nw;
   const int64_t w0 = t0 + warp * each + min((int64_t)warp, over);
   const int64_t w1 = warp < nw ? w0 + each + (warp < over ? 1 : 0) : w0;
   const int n = (int)(w1 - w0);
@@ -269,12 +287,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       Tile t{};
       const int64_t x = w0 + (int64_t)b * 32 + lane;
       if (x >= w1) return t;
-      int r = 0;
-      for (int hi = R; hi - r > 1;) {  // the last row with first[row] HC <= x
-        const int mid = (r + hi) >> 1;
-        if (sh.first[mid] * HC <= x) r = mid;
-        else hi = mid;
-      }
+      const int r = row_of(x);
       const int nt = (int)(sh.first[r + 1] - sh.first[r]);
       const int64_t rem = x - sh.first[r] * HC;
       t.hc = rem < nt ? 0 : (int)quick_div(rem, nt);
@@ -315,7 +328,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     // ---- loads, S - 1 tiles ahead of the products --------------------------------------------------
     const int lt = lane / CH, lc = lane % CH;  // a lane's token and chunk within a step of 32 chunks
     constexpr int kStep = 32 / CH;             // tokens of such a step
-    const bool mine = lc * 8 < D;
+    const bool copies = lc * 8 < D;
     // Pages of other sizes: the page of each token of a tile, copied to shared memory S tiles before
     // the tile's own copies start (with the copies of a tile that is waited for before that).
     auto look_up = [&](int i) {
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         const int64_t off = __shfl_sync(~0u, b.off, i & 31);
         const uint32_t seen = __shfl_sync(~0u, b.seen, i & 31);
         if (lane == 0) sh.seen[warp][slot] = seen;
-        if (mine) {
+        if (copies) {
           const int64_t at = off + (int64_t)lt * p.c.token_stride + lc * 8;
           const uint16_t *pk = p.k + at, *pv = p.v + at;
           const int64_t step = kStep * p.c.token_stride;
@@ -367,7 +380,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
           const int64_t o = __shfl_sync(~0u, off, t) + lc * 8;
           const uint32_t bytes = (seen >> t) & 1u ? 16u : 0u;
           uint16_t *dst = ks + t * DP + ((lc ^ (t & 7)) * 8);
-          if (mine) {
+          if (copies) {
             tc::cp_async16(dst, p.k + (bytes ? o : 0), bytes);
             tc::cp_async16(dst + kTile * DP, p.v + (bytes ? o : 0), bytes);
           }
@@ -580,103 +593,111 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
   if (!__syncthreads_or(pieces)) return;
 
   // ---- join the pieces of the CTA's warps, then those of the CTAs ------------------------------------
-  // Runs of pieces of one (row, head), in the order of the list: lane e looks at piece e. A run that began in
-  // an earlier CTA (the first) goes to the CTA's partial result 0, one that goes on in a later one (the
-  // last) to 1, the others to the output.
-  if (warp == 0) {
-    const int r = lane < 2 * nw ? sh.piece_row[lane] : -1, c = lane < 2 * nw ? sh.piece_hc[lane] : 0;
-    const uint32_t any = __ballot_sync(~0u, r >= 0);
+  // Every warp finds the runs of pieces of one (row, head) (lane e looks at piece e) and joins some of their
+  // heads. A run that began in an earlier CTA, and one that goes on in a later one, become the CTA's
+  // partial results 0 and 1; the others are done.
+  const int my_row = lane < 2 * nw ? sh.piece_row[lane] : -1, my_hc = lane < 2 * nw ? sh.piece_hc[lane] : 0;
+  const uint32_t any = __ballot_sync(~0u, my_row >= 0);
+  uint32_t starts;
+  {
     const uint32_t below = any & ((1u << lane) - 1u);
     const int before = below ? 31 - __clz(below) : 0;
-    const int r0 = __shfl_sync(~0u, r, before), c_before = __shfl_sync(~0u, c, before);
-    const bool starts = r >= 0 && (!below || r0 != r || c_before != c);
-    const uint32_t all = __ballot_sync(~0u, starts);
-    if (r >= 0) sh.order[__popc(below)] = lane;
-    if (starts) {
-      const uint32_t later = lane == 31 ? 0u : all >> (lane + 1);
-      const uint32_t until = later ? any & ((2u << (lane + __ffs(later) - 1)) - 1u) : any;
-      auto &run = sh.run[__popc(all & ((1u << lane) - 1u))];
-      run.from = __popc(below);
-      run.to = __popc(until);
-      run.row = r;
-      run.hc = c;
-      const int64_t nt = sh.first[r + 1] - sh.first[r], begin = sh.first[r] * HC + c * nt;
-      run.here = begin >= t0;
-      run.done = run.here && begin + nt <= t1;
-      int64_t head0;
-      run.heads = heads_of(c, head0);
-      run.out = run.done ? ((int64_t)p.row0 + r) * a.ldo + head0 * D : run.here * (int64_t)partial_floats(DP);
-    }
-    if (lane == 0) sh.runs = __popc(all);
+    const int r0 = __shfl_sync(~0u, my_row, before), c_before = __shfl_sync(~0u, my_hc, before);
+    starts = __ballot_sync(~0u, my_row >= 0 && (!below || r0 != my_row || c_before != my_hc));
   }
-  __syncthreads();
-  const int runs = sh.runs;
-  auto lse_of = [&](float m, float l) { return l == 0.f ? -CUDART_INF_F : (m - kShift) * CUDART_LN2_F + logf(l); };
-  // a run's maximum and sum, and from them each piece's weight
-  for (int i = tid; i < runs * GP; i += NT) {
-    const auto &run = sh.run[i / GP];
-    const int head = i % GP;
-    if (head >= run.heads) continue;
-    float top = -CUDART_INF_F, sum = 0.f;
-    for (int k = run.from; k < run.to; ++k) top = fmaxf(top, sh.m[sh.order[k]][head]);
-    const float base = top == -CUDART_INF_F ? 0.f : top;
-    for (int k = run.from; k < run.to; ++k) {
-      const int e = sh.order[k];
-      sum += exp2_fast(sh.m[e][head] - base) * sh.l[e][head];
-    }
-    const float inv = !run.done ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-    for (int k = run.from; k < run.to; ++k) {
-      const int e = sh.order[k];
-      sh.m[e][head] = exp2_fast(sh.m[e][head] - base) * inv;
-    }
-    if (run.done) {
-      int64_t head0;
-      heads_of(run.hc, head0);
-      if (a.lse) a.lse[((int64_t)p.row0 + run.row) * a.num_q_heads + head0 + head] = lse_of(top, sum);
-    } else {
-      float *to = partials + run.out + kMaxGroup * DP + head;
-      to[0] = top, to[16] = sum;
-    }
-  }
-  __syncthreads();
   auto pack4 = [&](float4 f) {
     uint2 u;
     u.x = (uint32_t)Elem<DT>::from_float(f.x) | ((uint32_t)Elem<DT>::from_float(f.y) << 16);
     u.y = (uint32_t)Elem<DT>::from_float(f.z) | ((uint32_t)Elem<DT>::from_float(f.w) << 16);
     return u;
   };
-  constexpr int kUnits = GP * (DP / 4);  // four elements of a head
-#pragma unroll 2
-  for (int x = tid; x < runs * kUnits; x += NT) {
-    const auto &run = sh.run[x / kUnits];
-    const int i = x % kUnits, head = i / (DP / 4), d = (i % (DP / 4)) * 4;
-    if (head >= run.heads) continue;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = run.from; k < run.to; ++k) {
-      const int e = sh.order[k];
-      const float w = sh.m[e][head];
-      const float4 f = (e & 1 ? reinterpret_cast<const float4 *>(sh.ring[e >> 1])
-                              : reinterpret_cast<const float4 *>(sh.head[e >> 1][0]))[i];
-      acc.x += w * f.x, acc.y += w * f.y, acc.z += w * f.z, acc.w += w * f.w;
+  auto lse_of = [&](float m, float l) { return l == 0.f ? -CUDART_INF_F : (m - kShift) * CUDART_LN2_F + logf(l); };
+  auto warp_max = [&](float x) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
+    return x;
+  };
+  auto warp_sum = [&](float x) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
+    return x;
+  };
+  // of the run that this lane's piece belongs to
+  const bool valid = my_row >= 0;
+  const int lead = valid ? 31 - __clz(starts & ((2u << lane) - 1u)) : 0;
+  const uint32_t later = lane == 31 ? 0u : starts >> (lane + 1);
+  const uint32_t run = valid ? any & (~0u << lead) & (later ? (2u << (lane + __ffs(later) - 1)) - 1u : ~0u) : 0u;
+  bool here = false, done = false;
+  int heads = 0;
+  int64_t head0 = 0;
+  if (valid) {
+    const int64_t nt = sh.first[my_row + 1] - sh.first[my_row], begin = sh.first[my_row] * HC + my_hc * nt;
+    here = begin >= t0, done = here && begin + nt <= t1;
+    heads = heads_of(my_hc, head0);
+  }
+  const int64_t my_out = done ? ((int64_t)p.row0 + my_row) * a.ldo + head0 * D : here * (int64_t)partial_floats(DP);
+  for (int head = warp; head < GP; head += NW) {
+    float top = -CUDART_INF_F, sum = 0.f, w = 0.f;
+    if (head < heads) {
+      for (uint32_t left = run; left; left &= left - 1) top = fmaxf(top, sh.m[__ffs(left) - 1][head]);
+      const float base = top == -CUDART_INF_F ? 0.f : top;
+      for (uint32_t left = run; left; left &= left - 1) {
+        const int e = __ffs(left) - 1;
+        sum += exp2_fast(sh.m[e][head] - base) * sh.l[e][head];
+      }
+      w = exp2_fast(sh.m[lane][head] - base);
+      if (done) w *= sum == 0.f ? 0.f : 1.f / sum;
+      if (lane == lead) {
+        if (!done) {
+          float *to = partials + my_out + kMaxGroup * DP + head;
+          to[0] = top, to[16] = sum;
+        } else if (a.lse) {
+          a.lse[((int64_t)p.row0 + my_row) * a.num_q_heads + head0 + head] = lse_of(top, sum);
+        }
+      }
     }
-    if (run.done) {
-      if (d < D) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + run.out + head * D + d) = pack4(acc);
-    } else {
-      *reinterpret_cast<float4 *>(partials + run.out + head * DP + d) = acc;
+    for (uint32_t todo = starts; todo; todo &= todo - 1) {
+      const int at = __ffs(todo) - 1;
+      const uint32_t pieces_of = __shfl_sync(~0u, run, at);
+      const int flags = __shfl_sync(~0u, heads * 2 + (done ? 1 : 0), at);
+      const int64_t out = __shfl_sync(~0u, my_out, at);
+      if (head >= flags >> 1) continue;
+#pragma unroll
+      for (int i0 = 0; i0 < DP / 4; i0 += 32) {
+        const int i = i0 + lane;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (uint32_t left = pieces_of; left; left &= left - 1) {
+          const int e = __ffs(left) - 1;
+          const float x = __shfl_sync(~0u, w, e);
+          if (i < DP / 4) {
+            const float4 f = reinterpret_cast<const float4 *>(e & 1 ? reinterpret_cast<const float *>(sh.ring[e >> 1])
+                                                                    : sh.head[e >> 1][0])[head * (DP / 4) + i];
+            acc.x += x * f.x, acc.y += x * f.y, acc.z += x * f.z, acc.w += x * f.w;
+          }
+        }
+        if (i >= DP / 4) continue;
+        if (!(flags & 1)) reinterpret_cast<float4 *>(partials + out)[head * (DP / 4) + i] = acc;
+        else if (i * 4 < D) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + out + head * D + i * 4) = pack4(acc);
+      }
     }
   }
-  // The items this CTA shares with others: the run that began before it, and the one that goes on behind it.
-  int open[2] = {-1, -1};
-  if (runs && !sh.run[0].here) open[0] = 0;
-  if (runs && sh.run[runs - 1].here && !sh.run[runs - 1].done) open[1] = runs - 1;
-  if (open[0] < 0 && open[1] < 0) return;
+  int open_row[2] = {-1, -1}, open_hc[2];
+  {
+    const int one = __ffs(starts) - 1, end = 31 - __clz(starts);  // the first and the last run
+    const int flags = (here ? 1 : 0) | (done ? 2 : 0);
+    if (!(__shfl_sync(~0u, flags, one) & 1)) open_row[0] = __shfl_sync(~0u, my_row, one);
+    open_hc[0] = __shfl_sync(~0u, my_hc, one);
+    if (__shfl_sync(~0u, flags, end) == 1) open_row[1] = __shfl_sync(~0u, my_row, end);
+    open_hc[1] = __shfl_sync(~0u, my_hc, end);
+  }
+  if (open_row[0] < 0 && open_row[1] < 0) return;
   __syncthreads();
-  int c0[2], c1[2];  // first and last CTA of such an item
+  int c0[2], c1[2];  // first and last CTA of the items this CTA shares with others
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if (open[h] < 0) continue;
-    const int r = sh.run[open[h]].row;
-    const int64_t nt = sh.first[r + 1] - sh.first[r], begin = sh.first[r] * HC + sh.run[open[h]].hc * nt;
+    if (open_row[h] < 0) continue;
+    const int r = open_row[h];
+    const int64_t nt = sh.first[r + 1] - sh.first[r], begin = sh.first[r] * HC + open_hc[h] * nt;
     c0[h] = cta_of(begin);
     c1[h] = cta_of(begin + nt - 1);
   }
@@ -684,7 +705,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     __threadfence();  // the CTA's partial results (seen here by the barrier) before the count
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (open[h] >= 0) {
+      if (open_row[h] >= 0) {
         const int before = atomicAdd(p.counters + c0[h], 1);
         sh.last[h] = before == c1[h] - c0[h];
         if (sh.last[h]) p.counters[c0[h]] = 0;  // nobody else comes: back to zero for the next call
@@ -694,67 +715,59 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
   __syncthreads();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if (open[h] < 0 || !sh.last[h]) continue;
-    const auto &run = sh.run[open[h]];
+    if (open_row[h] < 0 || !sh.last[h]) continue;
     const int count = c1[h] - c0[h] + 1;
     auto at = [&](int k) {
       return p.partials + ((int64_t)(c0[h] + k) * kPartialSlots + (k == 0 ? 1 : 0)) * partial_floats(DP);
     };
-    float4 early[4] = {};  // few partial results: all on their way at once
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k < count && tid < kUnits && tid / (DP / 4) < run.heads)
-        early[k] = __ldcg(reinterpret_cast<const float4 *>(at(k)) + tid);
-    float *w = reinterpret_cast<float *>(sh.ring[0]), *l = w + count * GP;  // [count][GP], in the idle ring
-    for (int i = tid; i < count * GP; i += NT) {
-      const float *x = at(i / GP) + kMaxGroup * DP + i % GP;
-      w[i] = __ldcg(x);
-      l[i] = __ldcg(x + 16);
-    }
-    __syncthreads();
-    if (tid < GP) {
+    int64_t h0;
+    const int hn = heads_of(open_hc[h], h0);
+    const int64_t row = (int64_t)p.row0 + open_row[h];
+    for (int head = warp; head < hn; head += NW) {
+      // 32 partial results at a time, lane j at the j-th; their m and l, and the first ones' elements, at once
       float top = -CUDART_INF_F, sum = 0.f;
-      for (int k = 0; k < count; ++k) top = fmaxf(top, w[k * GP + tid]);
-      const float base = top == -CUDART_INF_F ? 0.f : top;
-      for (int k = 0; k < count; ++k) {
-        const float f = exp2_fast(w[k * GP + tid] - base);
-        sum += f * l[k * GP + tid];
-        w[k * GP + tid] = f;
-      }
-      sh.top[tid] = top;
-      sh.sum[tid] = sum;
-    }
-    __syncthreads();
-    int64_t head0;
-    heads_of(run.hc, head0);
-    const int64_t row = (int64_t)p.row0 + run.row;
-    for (int i = tid; i < kUnits; i += NT) {
-      const int head = i / (DP / 4), d = (i % (DP / 4)) * 4;
-      if (head >= run.heads) break;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](float x, const float4 &f) {
-        acc.x += x * f.x, acc.y += x * f.y, acc.z += x * f.z, acc.w += x * f.w;
-      };
-      int k = 0;
-      if (i == tid)
+      float4 acc[(DP + 127) / 128] = {};
+      for (int k0 = 0; k0 < count; k0 += 32) {
+        const int kn = min(32, count - k0);
+        float m = -CUDART_INF_F, l = 0.f;
+        if (lane < kn) {
+          const float *x = at(k0 + lane) + kMaxGroup * DP + head;
+          m = __ldcg(x), l = __ldcg(x + 16);
+        }
+        const float before = top;
+        top = fmaxf(top, warp_max(m));
+        const float base = top == -CUDART_INF_F ? 0.f : top, keep = exp2_fast(before - base);
+        const float w = exp2_fast(m - base);
+        sum = sum * keep + warp_sum(w * l);
 #pragma unroll
-        for (; k < 4; ++k)
-          if (k < count) add(w[k * GP + head], early[k]);
-#pragma unroll 8
-      for (; k < count; ++k) add(w[k * GP + head], __ldcg(reinterpret_cast<const float4 *>(at(k)) + i));
-      const float inv = sh.sum[head] == 0.f ? 0.f : 1.f / sh.sum[head];
-      acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-      if (d < D)
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * a.ldo + (head0 + head) * D + d) = pack4(acc);
-      if (a.lse && d == 0) a.lse[row * a.num_q_heads + head0 + head] = lse_of(sh.top[head], sh.sum[head]);
+        for (int i = 0; i < (DP + 127) / 128; ++i) {
+          acc[i].x *= keep, acc[i].y *= keep, acc[i].z *= keep, acc[i].w *= keep;
+          const int j = i * 32 + lane;
+          const bool on = j < DP / 4;
+#pragma unroll 16
+          for (int k = 0; k < kn; ++k) {
+            const float4 f = on ? __ldcg(reinterpret_cast<const float4 *>(at(k0 + k)) + head * (DP / 4) + j)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float x = __shfl_sync(~0u, w, k);
+            acc[i].x += x * f.x, acc[i].y += x * f.y, acc[i].z += x * f.z, acc[i].w += x * f.w;
+          }
+        }
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+      for (int i = 0; i < (DP + 127) / 128; ++i) {
+        acc[i].x *= inv, acc[i].y *= inv, acc[i].z *= inv, acc[i].w *= inv;
+        const int j = i * 32 + lane;
+        if (j < DP / 4 && j * 4 < D)
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * a.ldo + (h0 + head) * D + j * 4) = pack4(acc[i]);
+      }
+      if (a.lse && lane == 0) a.lse[row * a.num_q_heads + h0 + head] = lse_of(top, sum);
     }
-    __syncthreads();  // the other item uses the same places
   }
 }
 
-// One per SM; at most as many as the weights of their partial results fit in a warp's ring.
-int attn_ctas() { return min(sm_count(), 192); }
-constexpr size_t kCounterBytes = 4096;  // more than any GPU's SMs
+constexpr size_t kCounterBytes = 4096;
+int attn_ctas() { return min(sm_count(), (int)(kCounterBytes / sizeof(int32_t))); }  // one per SM
 
 template <int DT, int DP, int NB, bool PAGED16>
 cudaError_t launch(const AttnParams &p, int32_t *status, cudaStream_t stream) {

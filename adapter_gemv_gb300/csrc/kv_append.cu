@@ -49,6 +49,7 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float
 template <int DT>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendParams p, int32_t *status) {
   pdl_wait();
+  pdl_launch_dependents();
   const mlora_kv_rows &r = p.r;
   const int D = p.c.head_dim, hq = r.num_q_heads, hk = p.c.num_kv_heads;
   const int row = blockIdx.y;

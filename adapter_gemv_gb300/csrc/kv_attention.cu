@@ -773,8 +773,7 @@ template <int DT, int DP, int NB, bool PAGED16>
 cudaError_t launch(const AttnParams &p, int32_t *status, cudaStream_t stream) {
   using Smem = AttnSmem<DP, attn_warps(DP), NB>;
   static_assert(sizeof(Smem) <= 227 * 1024, "fits in shared memory");
-  cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<DT, DP, NB, PAGED16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(Smem));
+  cudaError_t e = raise_smem<kv_attention_kernel<DT, DP, NB, PAGED16>>((int)sizeof(Smem));
   if (e != cudaSuccess) return e;
   e = launch_waiting(kv_attention_kernel<DT, DP, NB, PAGED16>, dim3(attn_ctas()), dim3(attn_warps(DP) * 32), sizeof(Smem), 1,
                      stream, p, status);

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(const __grid_consta
   int32_t *pages = rows + R + 1, *back = pages + R + 1, *len = back + R + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
   pdl_wait();
+  pdl_launch_dependents();
   const int64_t head = b.free_state[0], count = b.free_state[1];
   int bad = 0;
   // thread t holds requests t*each .. t*each+each-1
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(const __grid_consta
 cudaError_t launch_kv_layout(const mlora_kv_batch &b, int32_t *status, cudaStream_t stream) {
   const size_t smem = sizeof(LayoutSmem) + (size_t)(4 * b.num_requests + 3) * sizeof(int32_t);
   static_assert(sizeof(LayoutSmem) + (4 * MLORA_KV_MAX_REQUESTS + 3) * 4 <= 227 * 1024, "the sums fit in shared memory");
-  cudaError_t e = cudaFuncSetAttribute(kv_layout_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  cudaError_t e = raise_smem<kv_layout_kernel>(227 * 1024);
   if (e != cudaSuccess) return e;
   const int cluster = 8;
   e = launch_waiting(kv_layout_kernel, dim3(cluster), dim3(kThreads), smem, cluster, stream, b, fast_div(b.page_tokens),

@@ -3,13 +3,20 @@
 // Elementwise over [rows][vocab] once the history is a count per token: 2 x 4 bytes a logit and a
 // mask bit against a handful of flops, so bound by memory for a batch and by latency for a row.
 //
-// A CTA takes a slice of one row's vocabulary. It starts the loads of its logits into registers, then
-// counts the history's tokens that fall in its slice in shared memory (whole-number atomics: the
-// order does not matter), and applies the formula to what it holds. Each CTA of a row reads the
-// whole history (at most some 16 KB, from L2 after the first), which is cheaper than a
-// counting kernel before this one or an array of counts in global memory.
-// A count word holds the occurrences past the prompt, and bit 31 for a token of the prompt. Of several
-// bias entries with one id the last has to win: the bias word is the largest entry number + 1.
+// A CTA takes a slice of one row's vocabulary and streams it through. Few of its tokens are in the
+// request's history or bias list, so those are kept out of the stream: it leaves them alone (a bit per token says
+// which), and they are worked out afterwards, a thread a token; so out may be logits. The stream then
+// needs few registers and small tables, and four CTAs share an SM: while one waits for its row's lengths, its
+// history or its counts, the others stream.
+// The tokens kept out are numbered by their place among the bits set (a prefix sum over the words), and have
+// their count (occurrences past the prompt, whole-number atomics: the order does not matter; bit 31 for a
+// token of the prompt) and bias (the entry's number + 1, then its value, as one 64-bit maximum: of several
+// with one id the last wins) in arrays by that number; more than kPlaces of them, of a long history, take
+// several turns. Each CTA of a row reads the whole history: at most some 16 KB, from L2 after the first.
+// Measured at 256 x 128001 fp32 with histories of 512 to 4096 tokens, lists of 300 and half the rows masked: 69 us
+// (43 without history, list and mask). Also tried there: a table entry for every token of the slice, its
+// logits held in registers until the counts were there, 88 us; the touched tokens adjusted in the stream, with
+// the counts before it, 75 to 82; a CTA's share as one long stretch, 76.
 //
 // Rows of an odd vocabulary start at any multiple of the element: a slice is cut where 16-byte
 // vectors are aligned in memory, counted from the aligned address before the row's start.
@@ -22,9 +29,6 @@
 namespace mlora {
 
 namespace {
-
-constexpr int kThreads = 256;
-constexpr uint32_t kInPrompt = 0x80000000u;
 
 template <int DT>
 struct Vec {  // a 16-byte vector of logits
@@ -49,24 +53,74 @@ struct Vec<MLORA_FP32> {
   static __device__ __forceinline__ T put(float f) { return f; }
 };
 
-template <int DT, int NV>  // NV vectors a thread
-__global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant__ mlora_logits p, int32_t row0,
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kGroup = 4;    // vectors of a thread that are loaded together
+constexpr int kEarly = 4;    // tokens of the history that a thread loads ahead
+constexpr int kPlaces = 1024;
+constexpr uint32_t kInPrompt = 0x80000000u;
+
+template <int SLICE>
+struct LogitsSmem {
+  static constexpr int kWords = SLICE / 32;
+  uint32_t grammar[kWords + 1];  // the mask's bits of the slice, from the word of its first token
+  uint32_t hit[kWords];          // tokens of the history or the list
+  uint32_t before[kWords];       // how many of them in earlier words
+  uint32_t count[kPlaces], place[kPlaces];
+  unsigned long long bias[kPlaces];
+  uint32_t warp_sum[kWarps];
+};
+
+template <int DT, int G>  // G groups of vectors a thread; G = 0: one vector
+__global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_constant__ mlora_logits p, int32_t row0,
                                                           int32_t *status) {
   using V = Vec<DT>;
   using T = typename V::T;
-  constexpr int kSlice = kThreads * NV * V::N;
-  extern __shared__ __align__(16) uint32_t tab[];  // [kSlice] counts (with a history), [kSlice] biases (with a list)
+  constexpr int kVecs = G ? G * kGroup : 1, kLoad = G ? kGroup : 1;
+  constexpr int kSlice = kThreads * kVecs * V::N;
+  using Smem = LogitsSmem<kSlice>;
+  __shared__ Smem sh;
   pdl_wait();
-  const int tid = threadIdx.x, slice = blockIdx.x;
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slice = blockIdx.x;
   const int64_t row = (int64_t)row0 + blockIdx.y;
   int bad = 0;
   const int r = p.row_request ? p.row_request[row] : (int)row;
   if (r < -1 || r >= p.num_requests) bad |= MLORA_STATUS_BAD_REQUEST;
+  const T *src = static_cast<const T *>(p.logits) + row * p.ld;
+  T *dst = static_cast<T *>(p.out) + row * p.ldo;
+  const int skew = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));  // elements before the row's start
+  const bool same_skew = (int)((reinterpret_cast<uintptr_t>(dst) & 15) / sizeof(T)) == skew;
+  const int first = slice * kSlice - skew;  // token of the slice's first place (below 0 in a skewed first slice)
+  if (r == -1 || first >= p.vocab) return;
+  const int low = max(first, 0), high = min(first + kSlice, p.vocab);  // the slice's tokens
+  const bool interior = low == first && high == first + kSlice;
+
+  // Vector i of a thread: a whole one inside the row as it is; else its elements inside, from the first bits on.
+  auto token_of = [&](int i) { return first + (i * kThreads + tid) * V::N; };
+  auto load = [&](int i) {
+    const int t = token_of(i);
+    if (interior || (t >= 0 && t + V::N <= p.vocab)) return ldg_u4(src + t);
+    float f[V::N];
+#pragma unroll
+    for (int e = 0; e < V::N; ++e) f[e] = (t + e >= 0 && t + e < p.vocab) ? V::get(src[t + e]) : 0.f;
+    return V::pack(f);
+  };
+  uint4 x[kLoad];
+#pragma unroll
+  for (int k = 0; k < kLoad; ++k) x[k] = load(k);
+
   int total = 0, prompt = 0, bias0 = 0, bias1 = 0, grammar = -1;
-  float rep = 1.f, pres = 0.f, freq = 0.f, temp = 0.f;
-  if (!bad && r >= 0) {
+  float rep = 1.f, pres = 0.f, freq = 0.f, temp = 1.f;
+  const int32_t *text = nullptr;
+  int early[kEarly] = {};
+  if (!bad) {
     if (p.total_len) {
       total = p.total_len[r], prompt = p.prompt_len[r];
+      text = p.tokens + (int64_t)r * p.tokens_stride;  // (the array's rows are tokens_stride long)
+#pragma unroll
+      for (int k = 0; k < kEarly; ++k)
+        if (k * kThreads + tid < p.tokens_stride) early[k] = text[k * kThreads + tid];
       if (total < 0 || total > p.tokens_stride || prompt < 0 || prompt > total) bad |= MLORA_STATUS_BAD_LENGTH;
     }
     if (p.bias_offsets) {
@@ -81,121 +135,185 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
     if (p.presence) pres = p.presence[r];
     if (p.frequency) freq = p.frequency[r];
     if (p.temperature) temp = p.temperature[r];
+    if (!(temp > 0.f)) temp = 1.f;
   }
-  if (bad && slice == 0 && tid == 0) report(status, bad);
-  if (bad || r < 0) return;
-
-  const T *src = static_cast<const T *>(p.logits) + row * p.ld;
-  T *dst = static_cast<T *>(p.out) + row * p.ldo;
-  const int skew = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));  // elements before the row's start
-  const bool same_skew = (int)((reinterpret_cast<uintptr_t>(dst) & 15) / sizeof(T)) == skew;
-  const int first = slice * kSlice - skew;  // token of the slice's first place (below 0 in a skewed first slice)
-  if (first >= p.vocab) return;
-
-  float x[NV][V::N];
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int t = first + (k * kThreads + tid) * V::N;
-    if (t >= 0 && t + V::N <= p.vocab) {
-      V::unpack(ldg_u4(src + t), x[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) x[k][e] = (t + e >= 0 && t + e < p.vocab) ? V::get(src[t + e]) : 0.f;
-    }
+  if (bad) {
+    if (slice == 0 && tid == 0) report(status, bad);
+    return;
   }
 
-  const bool counted = total > 0, biased = bias1 > bias0;
-  uint32_t *count = tab, *entry = tab + (p.total_len ? kSlice : 0);
-  if (counted || biased) {
-    for (int i = tid * 4; i < kSlice; i += kThreads * 4) {
-      if (counted) *reinterpret_cast<uint4 *>(count + i) = make_uint4(0, 0, 0, 0);
-      if (biased) *reinterpret_cast<uint4 *>(entry + i) = make_uint4(0, 0, 0, 0);
-    }
-    __syncthreads();
-    const int32_t *text = p.tokens + (int64_t)r * p.tokens_stride;
-    int wrong = 0;
-#pragma unroll 4
-    for (int i = tid; i < total; i += kThreads) {
-      const int t = text[i];
-      if ((uint32_t)t >= (uint32_t)p.vocab) {
-        wrong = MLORA_STATUS_BAD_TOKEN;
-        continue;
-      }
-      const uint32_t at = (uint32_t)(t - first);
-      if (at < (uint32_t)kSlice) {
-        if (i < prompt) atomicOr(count + at, kInPrompt);
-        else atomicAdd(count + at, 1u);
-      }
-    }
-    for (int i = bias0 + tid; i < bias1; i += kThreads) {
-      const int t = p.bias_token[i];
-      if ((uint32_t)t >= (uint32_t)p.vocab) {
-        wrong = MLORA_STATUS_BAD_TOKEN;
-        continue;
-      }
-      const uint32_t at = (uint32_t)(t - first);
-      if (at < (uint32_t)kSlice) atomicMax(entry + at, (uint32_t)(i - bias0) + 1u);
-    }
-    if (wrong && slice == 0) report(status, wrong);
-    __syncthreads();
-  }
-
+  // ---- which tokens of the slice are in the history or the list --------------------------------------
+  const int listed = bias1 - bias0;
+  const int early_bias = tid < listed ? p.bias_token[bias0 + tid] : 0;
+  const float early_value = tid < listed ? p.bias_value[bias0 + tid] : 0.f;
+  const bool touched = total > 0 || listed > 0;
   const uint32_t *bits = grammar >= 0 ? p.mask + grammar * p.mask_stride : nullptr;
+  const int word0 = first >> 5, last_word = (p.vocab - 1) >> 5;  // (first may be below 0)
+  if (bits)
+    for (int i = tid; i <= Smem::kWords; i += kThreads) sh.grammar[i] = bits[min(max(word0 + i, 0), last_word)];
+  auto inside = [&](int t) { return (uint32_t)(t - low) < (uint32_t)(high - low); };
+  auto each_token = [&](auto f) {  // of the history, with its place in it
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int at = (k * kThreads + tid) * V::N, t = first + at;
+    for (int k = 0; k < kEarly; ++k)
+      if (k * kThreads + tid < total) f(k * kThreads + tid, early[k]);
+#pragma unroll 4
+    for (int i = kEarly * kThreads + tid; i < total; i += kThreads) f(i, text[i]);
+  };
+  auto each_entry = [&](auto f) {  // of the list, with its value
+    if (tid < listed) f(tid, early_bias, early_value);
+    for (int i = kThreads + tid; i < listed; i += kThreads) f(i, p.bias_token[bias0 + i], p.bias_value[bias0 + i]);
+  };
+  int kept = 0;  // how many tokens
+  // counts and biases of the tokens numbered from .. from + kPlaces - 1
+  auto number = [&](int t) {
+    const uint32_t at = (uint32_t)(t - first), w = at >> 5;
+    return sh.before[w] + __popc(sh.hit[w] & ((1u << (at & 31)) - 1u));
+  };
+  auto count_from = [&](int from) {
+    const uint32_t n = (uint32_t)min(kPlaces, kept - from);
+    for (int j = tid; j < (int)n; j += kThreads) sh.count[j] = 0, sh.bias[j] = 0;
+    __syncthreads();
+    each_token([&](int i, int t) {
+      if (!inside(t)) return;
+      const uint32_t j = number(t) - (uint32_t)from;
+      if (j >= n) return;
+      sh.place[j] = (uint32_t)(t - first);
+      if (i < prompt) atomicOr(&sh.count[j], kInPrompt);
+      else atomicAdd(&sh.count[j], 1u);
+    });
+    each_entry([&](int i, int t, float value) {
+      if (!inside(t)) return;
+      const uint32_t j = number(t) - (uint32_t)from;
+      if (j >= n) return;
+      sh.place[j] = (uint32_t)(t - first);
+      atomicMax(&sh.bias[j], ((unsigned long long)(i + 1) << 32) | __float_as_uint(value));
+    });
+    __syncthreads();
+  };
+  auto adjusted = [&](float f, int j) {  // before the temperature
+    const uint32_t c = sh.count[j], made = c & ~kInPrompt;
+    if (c) f = f > 0.f ? f / rep : f * rep;
+    if (made) f = f - freq * (float)made - pres;
+    const unsigned long long b = sh.bias[j];
+    return b ? f + __uint_as_float((uint32_t)b) : f;
+  };
+  if (touched) {
+    for (int i = tid; i < Smem::kWords; i += kThreads) sh.hit[i] = 0;
+    __syncthreads();
+    int wrong = 0;
+    auto mark = [&](int, int t) {
+      if (slice == 0 && (uint32_t)t >= (uint32_t)p.vocab) wrong = MLORA_STATUS_BAD_TOKEN;
+      if (inside(t)) atomicOr(&sh.hit[(t - first) >> 5], 1u << ((t - first) & 31));
+    };
+    each_token(mark);
+    each_entry([&](int i, int t, float) { mark(i, t); });
+    if (wrong) report(status, wrong);
+  }
+  if (touched || bits) __syncthreads();
+
+  // ---- the stream -------------------------------------------------------------------------------------
+#pragma unroll 1
+  for (int g = 0; g < (G ? G : 1); ++g) {
+    uint4 y[kLoad];
 #pragma unroll
-    for (int e = 0; e < V::N; ++e) {
-      float f = x[k][e];
-      if (counted) {
-        const uint32_t c = count[at + e];
-        if (c) f = f > 0.f ? f / rep : f * rep;
-        const uint32_t made = c & ~kInPrompt;
-        if (made) f = f - freq * (float)made - pres;
-      }
-      if (biased) {
-        const uint32_t b = entry[at + e];
-        if (b) f += p.bias_value[bias0 + b - 1];
-      }
-      if (temp > 0.f) f = f / temp;
-      if (bits && t + e >= 0 && t + e < p.vocab && !((bits[(t + e) >> 5] >> ((t + e) & 31)) & 1u)) f = -CUDART_INF_F;
-      x[k][e] = f;
+    for (int k = 0; k < kLoad; ++k) y[k] = x[k];
+    if (g + 1 < G) {
+#pragma unroll
+      for (int k = 0; k < kLoad; ++k) x[k] = load((g + 1) * kGroup + k);
     }
-    if (same_skew && t >= 0 && t + V::N <= p.vocab) {
-      *reinterpret_cast<uint4 *>(dst + t) = V::pack(x[k]);
-    } else {
 #pragma unroll
-      for (int e = 0; e < V::N; ++e)
-        if (t + e >= 0 && t + e < p.vocab) dst[t + e] = V::put(x[k][e]);
+    for (int k = 0; k < kLoad; ++k) {
+      const int i = g * kGroup + k, at = (i * kThreads + tid) * V::N, t = first + at;
+      float f[V::N];
+      V::unpack(y[k], f);
+      uint32_t allowed = ~0u;  // of the vector's tokens, from bit 0
+      if (bits)
+        allowed = __funnelshift_r(sh.grammar[(t >> 5) - word0], sh.grammar[((t + V::N - 1) >> 5) - word0], t & 31);
+      const uint32_t later = touched ? (sh.hit[at / 32] >> (at % 32)) & ((1u << V::N) - 1u) : 0u;
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) {
+        f[e] = f[e] / temp;
+        if (!(allowed >> e & 1u)) f[e] = -CUDART_INF_F;
+      }
+      if (same_skew && !later && (interior || (t >= 0 && t + V::N <= p.vocab))) {
+        *reinterpret_cast<uint4 *>(dst + t) = V::pack(f);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V::N; ++e)
+          if (!(later >> e & 1u) && t + e >= 0 && t + e < p.vocab) dst[t + e] = V::put(f[e]);
+      }
+    }
+  }
+  if (!touched) return;
+
+  // ---- the tokens kept out of it ------------------------------------------------------------------------
+  {
+    constexpr int kEach = (Smem::kWords + kThreads - 1) / kThreads;  // words a thread counts
+    uint32_t n = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (tid * kEach + k < Smem::kWords) n += __popc(sh.hit[tid * kEach + k]);
+    uint32_t incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(~0u, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    __syncthreads();
+    uint32_t at = incl - n, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += sh.warp_sum[w];
+      all += sh.warp_sum[w];
+    }
+    kept = (int)all;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (tid * kEach + k < Smem::kWords) {
+        sh.before[tid * kEach + k] = at;
+        at += __popc(sh.hit[tid * kEach + k]);
+      }
+  }
+  for (int from = 0; from < kept; from += kPlaces) {  // (one turn, but for long histories)
+    if (from) __syncthreads();
+    count_from(from);
+    for (int j = tid; j < min(kPlaces, kept - from); j += kThreads) {
+      const int t = first + (int)sh.place[j];
+      float f = adjusted(V::get(src[t]), j) / temp;
+      if (bits && !((sh.grammar[(t >> 5) - word0] >> (t & 31)) & 1u)) f = -CUDART_INF_F;
+      dst[t] = V::put(f);
     }
   }
 }
 
-template <int DT, int NV>
+template <int DT, int G>
 cudaError_t launch(const mlora_logits &a, int32_t *status, cudaStream_t stream) {
-  constexpr int kSlice = kThreads * NV * Vec<DT>::N;
-  const size_t smem = ((a.total_len ? 1 : 0) + (a.bias_offsets ? 1 : 0)) * kSlice * sizeof(uint32_t);
-  cudaError_t e = cudaFuncSetAttribute(logits_kernel<DT, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       2 * kSlice * (int)sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
+  constexpr int kSlice = kThreads * (G ? G * kGroup : 1) * Vec<DT>::N;
   // a row may start up to one vector's elements after an aligned address
   const int64_t slices = ((int64_t)a.vocab + Vec<DT>::N - 1 + kSlice - 1) / kSlice;
   for (int32_t row0 = 0; row0 < a.num_rows; row0 += 65535) {
     const dim3 grid((unsigned)slices, (unsigned)min(65535, a.num_rows - row0));
-    e = launch_waiting(logits_kernel<DT, NV>, grid, dim3(kThreads), smem, 1, stream, a, row0, status);
+    const cudaError_t e = launch_waiting(logits_kernel<DT, G>, grid, dim3(kThreads), 0, 1, stream, a, row0, status);
     if (e != cudaSuccess) return e;
     api_count_launch();
   }
   return cudaSuccess;
 }
 
+template <int DT>
+cudaError_t dispatch(const mlora_logits &a, int32_t *status, cudaStream_t stream) {
+  constexpr int G = DT == MLORA_FP32 ? 4 : 2;
+  if ((int64_t)a.num_rows * a.vocab < (int64_t)sm_count() * 4096) return launch<DT, 0>(a, status, stream);
+  return launch<DT, G>(a, status, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_logits_adjust(const mlora_logits &a, int32_t *status, cudaStream_t stream) {
   switch (a.dtype) {
-    case MLORA_FP32: return launch<MLORA_FP32, 4>(a, status, stream);
-    case MLORA_BF16: return launch<MLORA_BF16, 2>(a, status, stream);
-    default: return launch<MLORA_FP16, 2>(a, status, stream);
+    case MLORA_FP32: return dispatch<MLORA_FP32>(a, status, stream);
+    case MLORA_BF16: return dispatch<MLORA_BF16>(a, status, stream);
+    default: return dispatch<MLORA_FP16>(a, status, stream);
   }
 }
 

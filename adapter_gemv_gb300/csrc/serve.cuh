@@ -1,6 +1,8 @@
 // serve.cuh -- device helpers of the serving operators (sm_103a).
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "serve.h"
 
@@ -13,6 +15,19 @@ __device__ __forceinline__ int32_t div_by(const FastDiv &f, int32_t n) {
 
 // ceil(n / d), n >= 0
 __device__ __forceinline__ int32_t ceil_by(const FastDiv &f, int32_t n) { return n > 0 ? div_by(f, n - 1) + 1 : 0; }
+
+// Raise the dynamic shared memory that a kernel may be launched with, once per device.
+template <auto Kernel>
+inline cudaError_t raise_smem(int bytes) {
+  static std::atomic<bool> done[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
 
 // Launch with programmatic stream serialization: the CTAs may be placed while the kernel before them in
 // the stream ends. Every kernel launched this way calls pdl_wait() before its first access to

@@ -21,6 +21,9 @@ cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a,
 int64_t kv_attention_workspace_bytes(int32_t head_dim);
 cudaError_t launch_logits_adjust(const mlora_logits &a, int32_t *status, cudaStream_t stream);
 
+// Defined in decode_launch.cu: number of SMs of the current device.
+int sm_count();
+
 // n / d for 0 <= n < 2^31 and a divisor fixed per launch: a multiply-high and a shift (Granlund and
 // Montgomery, 1994).
 struct FastDiv {

@@ -172,3 +172,45 @@ def test_many_rows(dev):
     out = torch.empty_like(x)
     m.lora_logits_adjust(out, x, temperature=temp)
     assert torch.equal(out, x / temp[:, None])
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+@pytest.mark.parametrize("history, biases", [(33000, 5), (50, 70000), (33000, 140000), (32767, 65535)])
+def test_long_histories_and_lists(dev, rows, history, biases):
+    """Counts beyond 16 bits, and lists whose entry numbers are; many rows take the larger slices."""
+    a = make(2, 3001, torch.float32, history, biases)
+    a["total_len"][:] = history
+    a["tokens"][1, :] = 7  # one token all the way
+    a["prompt_len"][1] = 3
+    a["bias"] = (torch.tensor([0, biases, biases], dtype=torch.int32), torch.randint(0, 3001, (biases,)).to(torch.int32),
+                 torch.randn(biases))
+    want, tol = ref.logits(**a)
+    a["request"] = torch.arange(2, dtype=torch.int32).repeat(rows)
+    a["x"] = a["x"].repeat(rows, 1)
+    got = run(a, dev)
+    ref.assert_within(got, want.repeat(rows, 1), tol.repeat(rows, 1), "logits")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_large_batch_over_an_odd_vocabulary(dev, dtype):
+    a = make(3, 40001, dtype, 900, 30)
+    want, tol = ref.logits(**a)
+    a["request"] = torch.arange(3, dtype=torch.int32).repeat(40)
+    a["x"] = a["x"].repeat(40, 1)
+    for in_place in (False, True):
+        ref.assert_within(run(a, dev, in_place=in_place, pad=3), want.repeat(40, 1), tol.repeat(40, 1), "logits")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_temperatures_of_all_sizes(dev, dtype):
+    """Quotients at both ends of the range, infinities and zeros among the logits: what a division gives."""
+    temp = torch.tensor([1e-38, 1e-30, 1e-3, 0.1, 1 / 3, 1.0, 1.9999999, 3.0, 1e10, 1e30, 3e38, 2.0 ** -100, 1e-42], device=dev)
+    x = torch.randn((13, 5000), device=dev)
+    x[:, :8] = torch.tensor([0.0, -0.0, float("inf"), float("-inf"), 3e38, -3e38, 1e-38, 65504.0], device=dev)
+    x = x.to(dtype)
+    out = torch.empty_like(x)
+    m.lora_logits_adjust(out, x, temperature=temp)
+    want = (x.double() / temp.double()[:, None]).float().to(dtype)
+    tiny = want.float().abs() < 1e-37  # (rounded again below the normal numbers)
+    assert torch.equal(out[~tiny], want[~tiny])
+    assert ((out.double() - want.double()).abs()[tiny] <= 2e-45).all() or dtype != torch.float32

@@ -31,7 +31,6 @@ struct AppendParams {
   int64_t slots;        // num_pages * page_tokens
 };
 
-template <int DT>
 __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float *cs, const float *sn) {
   float c[8], s[8];
   *reinterpret_cast<float4 *>(c) = reinterpret_cast<const float4 *>(cs)[0];
@@ -46,73 +45,95 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float
   }
 }
 
-template <int DT>
+// A thread takes the same unit of ROWS rows, all loads on their way before the first store.
+template <int DT, int ROWS>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendParams p, int32_t *status) {
   pdl_wait();
   pdl_launch_dependents();
   const mlora_kv_rows &r = p.r;
-  const int D = p.c.head_dim, hq = r.num_q_heads, hk = p.c.num_kv_heads;
-  const int row = blockIdx.y;
+  const int D = p.c.head_dim, hq = r.num_q_heads, hk = p.c.num_kv_heads, half = r.rotary_dim >> 1;
   const int u = blockIdx.x * kThreads + threadIdx.x;
   if (u >= p.per_row.d) return;
-  const int64_t slot = r.cache_slot[row];
-  const int pos = r.rotary_dim ? r.position[row] : 0;
-  int bad = 0;
-  if (slot < -1 || slot >= p.slots) bad |= MLORA_STATUS_BAD_SLOT;
-  if (slot != -1 && r.rotary_dim && (pos < 0 || pos >= r.max_position)) bad |= MLORA_STATUS_BAD_LENGTH;
-  if (bad && u == 0) report(status, bad);
-  if (bad || slot < 0) return;
-
+  // the unit: which of q, k, v, its head, and the head's elements it covers (the first of them)
   const int rot_units = (hq + hk) * p.per_head.d;
-  const int64_t pg = slot / p.page.d;
-  const int64_t cell = pg * p.c.page_stride + (slot - pg * p.page.d) * p.c.token_stride;
-  if (u < rot_units) {
-    int h = div_by(p.per_head, u);
-    const int w = u - h * p.per_head.d;
-    const uint16_t *src;
-    uint16_t *dst;
-    if (h < hq) {
-      src = static_cast<const uint16_t *>(r.q) + row * r.ldq + (int64_t)h * D;
-      dst = static_cast<uint16_t *>(r.q_out) + row * r.ldq_out + (int64_t)h * D;
-    } else {
-      h -= hq;
-      src = static_cast<const uint16_t *>(r.k) + row * r.ldk + (int64_t)h * D;
-      dst = p.k + cell + h * p.c.head_stride;
-    }
-    const int half = r.rotary_dim >> 1;
-    if (w < p.pair_units) {
-      const int e = w * 8;
+  const bool is_v = u >= rot_units;
+  const FastDiv &per = is_v ? p.chunks : p.per_head;
+  const int w0 = is_v ? u - rot_units : u;
+  int h = div_by(per, w0);
+  const int w = w0 - h * per.d;
+  const bool is_q = !is_v && h < hq;
+  if (!is_v && !is_q) h -= hq;
+  const bool pairs = !is_v && w < p.pair_units;
+  const int e = (pairs || is_v ? w : w + p.pair_units) * 8;  // a pair unit holds two chunks
+  const bool turned = pairs || (!is_v && r.rope_interleaved && e < r.rotary_dim);
+  const uint16_t *src = static_cast<const uint16_t *>(is_v ? r.v : is_q ? r.q : r.k) + (int64_t)h * D + e;
+  const int64_t ld = is_v ? r.ldv : is_q ? r.ldq : r.ldk;
+
+  int64_t slot[ROWS];
+  int pos[ROWS];
+  const int row0 = blockIdx.y * ROWS;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int row = row0 + i;
+    slot[i] = row < r.num_rows ? r.cache_slot[row] : -1;
+    pos[i] = row < r.num_rows && r.rotary_dim ? r.position[row] : 0;
+  }
+  uint4 x[ROWS], y[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {  // (rows without a slot are read, too: their slot is not known yet)
+    if (row0 + i >= r.num_rows) continue;
+    x[i] = ldg_u4(src + (row0 + i) * ld);
+    if (pairs) y[i] = ldg_u4(src + (row0 + i) * ld + half);
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    int bad = 0;
+    if (slot[i] < -1 || slot[i] >= p.slots) bad |= MLORA_STATUS_BAD_SLOT;
+    if (slot[i] != -1 && r.rotary_dim && (pos[i] < 0 || pos[i] >= r.max_position)) bad |= MLORA_STATUS_BAD_LENGTH;
+    if (bad && u == 0) report(status, bad);
+    if (bad || slot[i] < 0) continue;
+    if (turned) {
+      const float *cs = r.rope_cos + (int64_t)pos[i] * half, *sn = r.rope_sin + (int64_t)pos[i] * half;
       float a[8], b[8];
-      unpack8<DT>(ldg_u4(src + e), a);
-      unpack8<DT>(ldg_u4(src + e + half), b);
-      rotate<DT>(a, b, r.rope_cos + (int64_t)pos * half + e, r.rope_sin + (int64_t)pos * half + e);
-      *reinterpret_cast<uint4 *>(dst + e) = pack8<DT>(a);
-      *reinterpret_cast<uint4 *>(dst + e + half) = pack8<DT>(b);
-    } else {
-      const int e = (w + p.pair_units) * 8;  // a pair unit holds two chunks
-      uint4 x = ldg_u4(src + e);
-      if (r.rope_interleaved && e < r.rotary_dim) {
-        float f[8];
-        unpack8<DT>(x, f);
-        const float4 c = *reinterpret_cast<const float4 *>(r.rope_cos + (int64_t)pos * half + e / 2);
-        const float4 s = *reinterpret_cast<const float4 *>(r.rope_sin + (int64_t)pos * half + e / 2);
+      unpack8<DT>(x[i], a);
+      if (pairs) {
+        unpack8<DT>(y[i], b);
+        rotate(a, b, cs + e, sn + e);
+        y[i] = pack8<DT>(b);
+      } else {
+        const float4 c = *reinterpret_cast<const float4 *>(cs + e / 2), s = *reinterpret_cast<const float4 *>(sn + e / 2);
         const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x0 = f[2 * i], x1 = f[2 * i + 1];
-          f[2 * i] = x0 * cc[i] - x1 * ss[i];
-          f[2 * i + 1] = x1 * cc[i] + x0 * ss[i];
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = a[2 * j], x1 = a[2 * j + 1];
+          a[2 * j] = x0 * cc[j] - x1 * ss[j];
+          a[2 * j + 1] = x1 * cc[j] + x0 * ss[j];
         }
-        x = pack8<DT>(f);
       }
-      *reinterpret_cast<uint4 *>(dst + e) = x;
+      x[i] = pack8<DT>(a);
     }
-  } else {
-    const int w = u - rot_units;
-    const int h = div_by(p.chunks, w), e = (w - h * p.chunks.d) * 8;
-    *reinterpret_cast<uint4 *>(p.v + cell + h * p.c.head_stride + e) =
-        ldg_u4(static_cast<const uint16_t *>(r.v) + row * r.ldv + (int64_t)h * D + e);
+    uint16_t *dst;
+    if (is_q) {
+      dst = static_cast<uint16_t *>(r.q_out) + (row0 + i) * r.ldq_out + (int64_t)h * D + e;
+    } else {
+      const int64_t pg = p.slots <= INT32_MAX ? div_by(p.page, (int32_t)slot[i]) : slot[i] / p.page.d;
+      dst = (is_v ? p.v : p.k) + pg * p.c.page_stride + (slot[i] - pg * p.page.d) * p.c.token_stride +
+            h * p.c.head_stride + e;
+    }
+    *reinterpret_cast<uint4 *>(dst) = x[i];
+    if (pairs) *reinterpret_cast<uint4 *>(dst + half) = y[i];
   }
+}
+
+template <int ROWS>
+cudaError_t launch(const AppendParams &p, int32_t *status, cudaStream_t stream) {
+  const dim3 grid((p.per_row.d + kThreads - 1) / kThreads, (p.r.num_rows + ROWS - 1) / ROWS);
+  const cudaError_t e =
+      p.c.dtype == MLORA_BF16
+          ? launch_waiting(kv_append_kernel<MLORA_BF16, ROWS>, grid, dim3(kThreads), 0, 1, stream, p, status)
+          : launch_waiting(kv_append_kernel<MLORA_FP16, ROWS>, grid, dim3(kThreads), 0, 1, stream, p, status);
+  if (e == cudaSuccess) api_count_launch();
+  return e;
 }
 
 }  // namespace
@@ -133,7 +154,7 @@ cudaError_t launch_kv_append(const mlora_kv_cache &c, const mlora_kv_rows &r, in
   p.per_row = fast_div((r.num_q_heads + c.num_kv_heads) * p.per_head.d + c.num_kv_heads * chunks);
   for (int32_t row0 = 0; row0 < r.num_rows; row0 += 65535) {
     AppendParams q = p;
-    const int n = min(65535, r.num_rows - row0);
+    q.r.num_rows = min(65535, r.num_rows - row0);
     q.r.cache_slot += row0;
     if (q.r.position) q.r.position += row0;
     q.r.k = static_cast<const uint16_t *>(r.k) + row0 * r.ldk;
@@ -142,12 +163,12 @@ cudaError_t launch_kv_append(const mlora_kv_cache &c, const mlora_kv_rows &r, in
       q.r.q = static_cast<const uint16_t *>(r.q) + row0 * r.ldq;
       q.r.q_out = static_cast<uint16_t *>(r.q_out) + row0 * r.ldq_out;
     }
-    const dim3 grid((p.per_row.d + kThreads - 1) / kThreads, n);
-    const cudaError_t e = c.dtype == MLORA_BF16
-                              ? launch_waiting(kv_append_kernel<MLORA_BF16>, grid, dim3(kThreads), 0, 1, stream, q, status)
-                              : launch_waiting(kv_append_kernel<MLORA_FP16>, grid, dim3(kThreads), 0, 1, stream, q, status);
+    // Two rows a thread where that still leaves every SM its eight CTAs: 12604 rows of 40 + 80 heads of 128 take
+    // 131 us so, 160 with a row each, 138 with four (5.9 TB/s of reads and writes; a copy reaches 6.7). 32
+    // rows: 2.3 us with a row each.
+    const cudaError_t e = (int64_t)q.r.num_rows * p.per_row.d >= (int64_t)sm_count() * 8 * kThreads * 2
+                              ? launch<2>(q, status, stream) : launch<1>(q, status, stream);
     if (e != cudaSuccess) return e;
-    api_count_launch();
   }
   return cudaSuccess;
 }

@@ -3,20 +3,22 @@
 // Elementwise over [rows][vocab] once the history is a count per token: 2 x 4 bytes a logit and a
 // mask bit against a handful of flops, so bound by memory for a batch and by latency for a row.
 //
-// A CTA takes a slice of one row's vocabulary and streams it through. Few of its tokens are in the
-// request's history or bias list, so those are kept out of the stream: it leaves them alone (a bit per token says
-// which), and they are worked out afterwards, a thread a token; so out may be logits. The stream then
-// needs few registers and small tables, and four CTAs share an SM: while one waits for its row's lengths, its
-// history or its counts, the others stream.
-// The tokens kept out are numbered by their place among the bits set (a prefix sum over the words), and have
+// A CTA takes a slice of one row's vocabulary and streams it through: temperature and mask, which need no
+// table. Few of its tokens are in the request's history or bias list; a bit per token says which, and they
+// are worked out behind the stream, a thread a token, from the logits as they came, over what the stream has
+// written there (where out is logits the stream leaves them alone: 69 us instead of 64 below, as vectors with such
+// a token go out in parts). So the stream needs few registers and small tables, and four CTAs share an SM:
+// while one waits for its row's lengths, its history or its counts, the others stream.
+// The touched tokens are numbered by their place among the bits set (a prefix sum over the words), and have
 // their count (occurrences past the prompt, whole-number atomics: the order does not matter; bit 31 for a
 // token of the prompt) and bias (the entry's number + 1, then its value, as one 64-bit maximum: of several
 // with one id the last wins) in arrays by that number; more than kPlaces of them, of a long history, take
 // several turns. Each CTA of a row reads the whole history: at most some 16 KB, from L2 after the first.
-// Measured at 256 x 128001 fp32 with histories of 512 to 4096 tokens, lists of 300 and half the rows masked: 69 us
-// (43 without history, list and mask). Also tried there: a table entry for every token of the slice, its
-// logits held in registers until the counts were there, 88 us; the touched tokens adjusted in the stream, with
-// the counts before it, 75 to 82; a CTA's share as one long stretch, 76.
+// Measured at 256 x 128001 fp32 with histories of 512 to 4096 tokens, lists of 300 and half the rows masked: 64 us,
+// 4.1 TB/s (43 us, 6.1 TB/s, without history, list and mask); it is the instructions around the tables, issued
+// in two of three cycles. Also tried there: a table entry for every token of the slice, its logits held in
+// registers until the counts were there, 88 us; the touched tokens adjusted in the stream, with the counts before
+// it, 75 to 82; a CTA's share as one long stretch, 76; a division replaced by a corrected product, no gain.
 //
 // Rows of an odd vocabulary start at any multiple of the element: a slice is cut where 16-byte
 // vectors are aligned in memory, counted from the aligned address before the row's start.
@@ -81,7 +83,6 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
   using Smem = LogitsSmem<kSlice>;
   __shared__ Smem sh;
   pdl_wait();
-  pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slice = blockIdx.x;
   const int64_t row = (int64_t)row0 + blockIdx.y;
   int bad = 0;
@@ -90,6 +91,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
   const T *src = static_cast<const T *>(p.logits) + row * p.ld;
   T *dst = static_cast<T *>(p.out) + row * p.ldo;
   const int skew = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));  // elements before the row's start
+  const bool in_place = dst == src;
   const bool same_skew = (int)((reinterpret_cast<uintptr_t>(dst) & 15) / sizeof(T)) == skew;
   const int first = slice * kSlice - skew;  // token of the slice's first place (below 0 in a skewed first slice)
   if (r == -1 || first >= p.vocab) return;
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
       uint32_t allowed = ~0u;  // of the vector's tokens, from bit 0
       if (bits)
         allowed = __funnelshift_r(sh.grammar[(t >> 5) - word0], sh.grammar[((t + V::N - 1) >> 5) - word0], t & 31);
-      const uint32_t later = touched ? (sh.hit[at / 32] >> (at % 32)) & ((1u << V::N) - 1u) : 0u;
+      const uint32_t later = touched && in_place ? (sh.hit[at / 32] >> (at % 32)) & ((1u << V::N) - 1u) : 0u;
 #pragma unroll
       for (int e = 0; e < V::N; ++e) {
         f[e] = f[e] / temp;
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
   }
   if (!touched) return;
 
-  // ---- the tokens kept out of it ------------------------------------------------------------------------
+  // ---- the touched tokens ------------------------------------------------------------------------------------
   {
     constexpr int kEach = (Smem::kWords + kThreads - 1) / kThreads;  // words a thread counts
     uint32_t n = 0;
@@ -302,9 +304,10 @@ cudaError_t launch(const mlora_logits &a, int32_t *status, cudaStream_t stream) 
 
 template <int DT>
 cudaError_t dispatch(const mlora_logits &a, int32_t *status, cudaStream_t stream) {
-  constexpr int G = DT == MLORA_FP32 ? 4 : 2;
+  // Slices of 16384 tokens; where that gives the SMs less than one each to do (at 4096 tokens an SM), slices of
+  // one vector a thread: a row of 32000 takes 3.4 us so, and 5.3 in slices of 4096.
   if ((int64_t)a.num_rows * a.vocab < (int64_t)sm_count() * 4096) return launch<DT, 0>(a, status, stream);
-  return launch<DT, G>(a, status, stream);
+  return launch<DT, DT == MLORA_FP32 ? 4 : 2>(a, status, stream);
 }
 
 }  // namespace

@@ -29,6 +29,8 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "serve.cuh"
 #include "tc.cuh"
 
@@ -43,6 +45,10 @@ constexpr int kMinTiles = 2;         // a warp's share of a small call, so that 
 // shares are at most kSmallShare tiles (above).
 constexpr int kSmallShare = 64, kWhole = 96, kWholeLarge = 24;
 constexpr int kMaxGroup = 16;        // query heads of a work item
+// Where a warp has at most this many tiles, the list holds an empty one behind every (row, head): what starting
+// and ending one costs, about a tile's products (0.5 us), counts beside the tiles then, not in a call that
+// waits for memory.
+constexpr int kFewTiles = 16;
 constexpr float kSlack = 8.f;        // log2 of how far a weight may pass 1 before m moves
 
 constexpr int attn_warps(int dp) { return dp == 256 ? 4 : 8; }
@@ -65,9 +71,7 @@ struct AttnParams {
 };
 
 // a / b for a >= 0, b > 0
-__device__ __forceinline__ int64_t quick_div(int64_t a, int64_t b) {
-  return ((uint64_t)(a | b) >> 32) ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
+__device__ __forceinline__ int quick_div(int a, int b) { return (int)((uint32_t)a / (uint32_t)b); }
 
 __device__ __forceinline__ float exp2_fast(float x) {  // ex2.approx: 2 ulp, exact limits
   float y;
@@ -128,10 +132,10 @@ __device__ __forceinline__ void cp_async_wait() {
 struct Tile {
   int64_t off;    // pages of whole tiles: its first token in the cache; else its request and first token
   uint32_t seen;  // bit t: token t is seen
-  uint32_t row;   // the row, with kFirst / kLast for the first / last tile of its (row, head)
+  uint32_t row;   // the row, with kFirst / kLast for the first / last tile of its (row, head), kNone for no tile
   int32_t hc;     // key-value head and chunk of its group
 };
-constexpr uint32_t kFirst = 1u << 30, kLast = 1u << 31, kRowMask = kFirst - 1;
+constexpr uint32_t kNone = 1u << 29, kFirst = 1u << 30, kLast = 1u << 31, kRowMask = kNone - 1;
 
 template <int DP, int NW, int NB>
 struct AttnSmem {
@@ -139,12 +143,13 @@ struct AttnSmem {
   static constexpr int kStageElems = 2 * kTile * DP;  // K, then V
   uint16_t ring[NW][kStages][kStageElems];  // a warp's tiles; after the last, its unfinished last piece
   float head[NW][NB * 8][DP];               // its unfinished first piece
-  int64_t first[kRowsPerLaunch + 1];        // tiles (of one head) before a row
+  int32_t first[kRowsPerLaunch + 1];        // tiles (of one head) before a row
   int32_t pos[kRowsPerLaunch];              // last token seen; -1: none, -2: a bad row
   int32_t req[kRowsPerLaunch];              // the row's request
   uint32_t seen[NW][kStages];               // bit t: token t of the tile is seen
-  int64_t warp_sum[NW];
+  int32_t warp_sum[NW], warp_rows[NW];
   int32_t page_id[NW][2 * kStages][kTile];  // pages of tokens, where a page does not hold whole tiles
+  int64_t at[NW][kTile];                    // and the tokens' places in the cache (-1: not seen)
   // pieces: [2w] without the first tile of its (row, head), [2w+1] with it
   float m[2 * NW][kMaxGroup], l[2 * NW][kMaxGroup];
   int32_t piece_row[2 * NW], piece_hc[2 * NW];
@@ -172,10 +177,10 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
   pdl_launch_dependents();
   // ---- the list of tiles: exclusive sums of the rows' tile counts ------------------------------
   const int R = p.rows;
+  int empty;  // 1: an empty tile behind every (row, head)
   {
     const int each = (R + NT - 1) / NT;
-    int64_t sum = 0;
-    int bad = 0;
+    int sum = 0, some = 0, bad = 0;  // tiles; rows that have any
     for (int i = 0; i < each; ++i) {
       const int r = tid * each + i;
       if (r >= R) break;
@@ -192,25 +197,31 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       sh.req[r] = req;
       sh.first[r] = n;
       sum += n;
+      some += n > 0;
     }
-    int64_t incl = sum;
+    int incl = sum, rows = some;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(~0u, incl, d);
-      if (lane >= d) incl += o;
+      const int x = __shfl_up_sync(~0u, incl, d), y = __shfl_up_sync(~0u, rows, d);
+      if (lane >= d) incl += x, rows += y;
     }
-    if (lane == 31) sh.warp_sum[warp] = incl;
+    if (lane == 31) sh.warp_sum[warp] = incl, sh.warp_rows[warp] = rows;
     if (bad && blockIdx.x == 0) report(status, bad);
     if (tid < 2 * NW) sh.piece_row[tid] = -1;
     __syncthreads();
-    int64_t at = incl - sum;
-    for (int w = 0; w < warp; ++w) at += sh.warp_sum[w];
+    int at = incl - sum, before = rows - some, all = 0;
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) at += sh.warp_sum[w], before += sh.warp_rows[w];
+      all += sh.warp_sum[w];
+    }
+    empty = (int64_t)all * HC <= (int64_t)gridDim.x * NW * kFewTiles ? 1 : 0;
+    at += empty * before;
     for (int i = 0; i < each; ++i) {
       const int r = tid * each + i;
       if (r >= R) break;
-      const int64_t n = sh.first[r];
+      const int n = sh.first[r];
       sh.first[r] = at;
-      at += n;
+      at += n ? n + empty : 0;
     }
     if (tid == NT - 1) sh.first[R] = at;
     __syncthreads();
@@ -227,17 +238,17 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
 
   // ---- this CTA's and this warp's part of it -----------------------------------------------------
   // Even shares: the first `rest` CTAs (warps) take a tile more.
-  const int64_t T = sh.first[R] * HC;
-  const int64_t shares = (T + kMinTiles - 1) / kMinTiles;
-  const int C = (int)min((int64_t)gridDim.x, shares);
+  const int T = sh.first[R] * HC;  // (below 2^31: the launcher sees to it)
+  const int C = min((int)gridDim.x, quick_div(T + kMinTiles - 1, kMinTiles));
   if ((int)blockIdx.x >= C) return;
-  const int64_t share = quick_div(T, C), rest = T - share * C;
-  auto first_of = [&](int64_t cta) { return cta * share + min(cta, rest); };
-  auto cta_of = [&](int64_t tile) {
-    return (int)(tile < rest * (share + 1) ? quick_div(tile, share + 1) : rest + quick_div(tile - rest * (share + 1), share));
+  const int share = quick_div(T, C), rest = T - share * C;
+  auto first_of = [&](int cta) { return cta * share + min(cta, rest); };
+  auto cta_of = [&](int tile) {
+    const int longer = rest * (share + 1);
+    return tile < longer ? quick_div(tile, share + 1) : rest + quick_div(tile - longer, share);
   };
   // the last row with first[row] HC <= x, for x < T
-  auto row_of = [&](int64_t x) {
+  auto row_of = [&](int x) {
     int r = 0;
     for (int hi = R; hi - r > 1;) {
       const int mid = (r + hi) >> 1;
@@ -246,26 +257,23 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     }
     return r;
   };
-  int64_t t0, t1;
+  int t0, t1;
   {
-    int64_t x = first_of(blockIdx.x + (lane & 1));  // lanes 0 and 1: the CTA's two boundaries
+    int x = first_of(blockIdx.x + (lane & 1));  // lanes 0 and 1: the CTA's two boundaries
     if (x < T) {
-      const int r = row_of(x);
-      const int nt = (int)(sh.first[r + 1] - sh.first[r]);
+      const int r = row_of(x), nt = sh.first[r + 1] - sh.first[r];
       if (nt <= (share <= kSmallShare ? kWhole : kWholeLarge)) {
-        const int64_t rem = x - sh.first[r] * HC;
-        const int in = (int)(rem - quick_div(rem, nt) * nt);
+        const int rem = x - sh.first[r] * HC, in = rem - quick_div(rem, nt) * nt;
         x += 2 * in < nt ? -in : nt - in;
       }
     }
     t0 = __shfl_sync(~0u, x, 0), t1 = __shfl_sync(~0u, x, 1);
   }
-  const int64_t mine = t1 - t0;
-  const int nw = mine >= (int64_t)NW * kMinTiles ? NW : max(1, (int)(mine + kMinTiles - 1) / kMinTiles);
-  const int64_t each = nw == NW ? mine / NW : quick_div(mine, nw), over = mine - each * nw;
-  const int64_t w0 = t0 + warp * each + min((int64_t)warp, over);
-  const int64_t w1 = warp < nw ? w0 + each + (warp < over ? 1 : 0) : w0;
-  const int n = (int)(w1 - w0);
+  const int mine = t1 - t0;
+  const int nw = min(NW, max(1, quick_div(mine + kMinTiles - 1, kMinTiles)));
+  const int each = quick_div(mine, nw), over = mine - each * nw;
+  const int w0 = t0 + warp * each + min(warp, over);
+  const int n = warp < nw ? each + (warp < over ? 1 : 0) : 0;
 
   // the query heads of an item: the first one's number, and how many
   auto heads_of = [&](int hc, int64_t &head0) {
@@ -273,6 +281,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     head0 = (int64_t)hk * p.group + g0;
     return min(p.group - g0, kMaxGroup);
   };
+  auto lse_of = [&](float m, float l) { return l == 0.f ? -CUDART_INF_F : (m - kShift) * CUDART_LN2_F + logf(l); };
   float *const partials = p.partials + (int64_t)blockIdx.x * kPartialSlots * partial_floats(DP);
   // chunks past the head's end are never copied: zero for good
   if (D < DP) {
@@ -285,22 +294,26 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     // tiles w0 + 32 b + lane
     auto place = [&](int b) {
       Tile t{};
-      const int64_t x = w0 + (int64_t)b * 32 + lane;
-      if (x >= w1) return t;
+      const int i = b * 32 + lane, x = w0 + i;
+      if (i >= n) return t;
       const int r = row_of(x);
-      const int nt = (int)(sh.first[r + 1] - sh.first[r]);
-      const int64_t rem = x - sh.first[r] * HC;
-      t.hc = rem < nt ? 0 : (int)quick_div(rem, nt);
-      const int tile = (int)(rem - (int64_t)t.hc * nt);
+      const int nt = sh.first[r + 1] - sh.first[r];
+      const int rem = x - sh.first[r] * HC;
+      t.hc = rem < nt ? 0 : quick_div(rem, nt);
+      const int tile = rem - t.hc * nt;
+      if (empty && tile == nt - 1) {
+        t.row = kNone;
+        return t;
+      }
       const int pos = sh.pos[r], lo = a.window ? max(0, pos + 1 - a.window) : 0;
       const int t0 = (lo / kTile + tile) * kTile;
       t.seen = 0xFFFFu;
       if (t0 < lo) t.seen &= 0xFFFFu << (lo - t0);
       if (pos - t0 < kTile - 1) t.seen &= (2u << (pos - t0)) - 1u;
-      t.row = (uint32_t)r | (tile == 0 ? kFirst : 0u) | (tile == nt - 1 ? kLast : 0u);
+      t.row = (uint32_t)r | (tile == 0 ? kFirst : 0u) | (tile == nt - 1 - empty ? kLast : 0u);
       const int64_t row = (int64_t)p.row0 + r;
       const int req = sh.req[r];
-      if (tile == 0 || x == w0) {  // q of the (row, head), into L2
+      if (tile == 0 || i == 0) {  // q of the (row, head), into L2
         int64_t head0;
         const int heads = heads_of(t.hc, head0);
         prefetch_l2(static_cast<const uint16_t *>(a.q) + row * a.ldq + head0 * D, (uint32_t)(heads * D * 2));
@@ -346,7 +359,8 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         const int64_t off = __shfl_sync(~0u, b.off, i & 31);
         const uint32_t seen = __shfl_sync(~0u, b.seen, i & 31);
         if (lane == 0) sh.seen[warp][slot] = seen;
-        if (copies) {
+        const bool none = (__shfl_sync(~0u, b.row, i & 31) & kNone) != 0;
+        if (copies && !none) {  // (a tile whose page is missing is filled with zeros)
           const int64_t at = off + (int64_t)lt * p.c.token_stride + lc * 8;
           const uint16_t *pk = p.k + at, *pv = p.v + at;
           const int64_t step = kStep * p.c.token_stride;
@@ -368,23 +382,27 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         const int id = want ? sh.page_id[warp][i % (2 * S)][lane & 15] : -1;
         const bool good = id >= 0 && id < p.c.num_pages;
         if (want && !good) report(status, MLORA_STATUS_BAD_PAGE);
-        const int64_t off = good ? (int64_t)id * p.c.page_stride +
-                                       (int64_t)(t0 - div_by(p.page, t0) * p.page.d) * p.c.token_stride +
-                                       (int64_t)(p.chunks == 1 ? hc : hc / p.chunks) * p.c.head_stride
-                                 : 0;
-        const uint32_t seen = __ballot_sync(~0u, good) & 0xFFFFu;
+        if (lane < kTile)
+          sh.at[warp][lane] = good ? (int64_t)id * p.c.page_stride +
+                                         (int64_t)(t0 - div_by(p.page, t0) * p.page.d) * p.c.token_stride +
+                                         (int64_t)(p.chunks == 1 ? hc : hc / p.chunks) * p.c.head_stride
+                                   : -1;
+        const uint32_t seen = __ballot_sync(~0u, good) & 0xFFFFu;  // (also orders at[] for the warp)
+        __syncwarp();
         if (lane == 0) sh.seen[warp][slot] = seen;
+        if (copies) {
 #pragma unroll
-        for (int j = 0; j < kTile / kStep; ++j) {
-          const int t = j * kStep + lt;
-          const int64_t o = __shfl_sync(~0u, off, t) + lc * 8;
-          const uint32_t bytes = (seen >> t) & 1u ? 16u : 0u;
-          uint16_t *dst = ks + t * DP + ((lc ^ (t & 7)) * 8);
-          if (copies) {
-            tc::cp_async16(dst, p.k + (bytes ? o : 0), bytes);
-            tc::cp_async16(dst + kTile * DP, p.v + (bytes ? o : 0), bytes);
+          for (int j = 0; j < kTile / kStep; ++j) {
+            const int t = j * kStep + lt;
+            const int64_t o = sh.at[warp][t];
+            const uint32_t bytes = o >= 0 ? 16u : 0u;
+            const int64_t from = o >= 0 ? o + lc * 8 : 0;
+            uint16_t *dst = ks + t * DP + ((lc ^ (t & 7)) * 8);
+            tc::cp_async16(dst, p.k + from, bytes);
+            tc::cp_async16(dst + kTile * DP, p.v + from, bytes);
           }
         }
+        __syncwarp();  // at[] may be written again
         if (i + S < n) look_up(i + S);
       }
     };
@@ -422,7 +440,6 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
           }
     };
     constexpr bool kAhead = DP * NB < 512;  // (no registers left for it at 16 heads of 256)
-    if constexpr (kAhead) load_q(0);
     float o[DP / 16][NB][4];     // O^T: elements j * 16 + g (0, 1) and + 8 (2, 3), heads quad * 2 + {0, 1}
     float m[NB][2], l[NB][2];    // of heads quad * 2 + {0, 1}; l: of this lane's tokens
     bool start = true, with_first = false;
@@ -432,6 +449,10 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     const int kt = lane & 15, kc = lane >> 4;
     const int vt = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
     int slot = 0;
+    {
+      const int skip = __shfl_sync(~0u, cur.row, 0) & kNone ? 1 : 0;
+      if (kAhead && skip < n) load_q(skip);
+    }
     for (int it = 0; it < n; ++it) {
       if ((it & 31) == 0 && it) {
         cur = nxt;
@@ -439,7 +460,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         if (it + 32 < n) nxt = place(cur_batch + 1);
       }
       const uint32_t meta = __shfl_sync(~0u, cur.row, it & 31);
-      if (start) {
+      if (start && !(meta & kNone)) {
         if constexpr (!kAhead) load_q(it);
         row_in = (int)(meta & kRowMask);
         hc = __shfl_sync(~0u, cur.hc, it & 31);
@@ -459,11 +480,16 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         }
         start = false;
       }
-      if (kAhead && (meta & kLast) && it + 1 < n) load_q(it + 1);  // the next tile begins another (row, head)
+      if (kAhead && (meta & kLast) && it + 1 + empty < n) load_q(it + 1 + empty);  // another (row, head)'s
       if (it + S - 1 < n) issue(it + S - 1, slot == 0 ? S - 1 : slot - 1);
       cp_async_commit();
       cp_async_wait<S - 1>();
       __syncwarp();
+      if (meta & kNone) {
+        if (++slot == S) slot = 0;
+        __syncwarp();
+        continue;
+      }
       const uint32_t seen = sh.seen[warp][slot];
       const uint32_t ks = smem_u32(sh.ring[warp][slot]), vs = ks + kTile * DP * 2;
 
@@ -546,22 +572,24 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
           }
         if ((meta & kLast) && with_first) {  // and whole
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+          for (int nb = 0; nb < NB; ++nb) {
+            float inv[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
+              inv[j] = l[nb][j] == 0.f ? 0.f : 1.f / l[nb][j];
               const int head = nb * 8 + quad * 2 + j;
-              if (head >= gn) continue;
-              const float inv = l[nb][j] == 0.f ? 0.f : 1.f / l[nb][j];
-              uint16_t *dst = static_cast<uint16_t *>(a.out) + row * a.ldo + (head0 + head) * D;
-#pragma unroll
-              for (int i = 0; i < DP / 16; ++i) {
-                if (i * 16 < D) dst[i * 16 + g] = Elem<DT>::from_float(o[i][nb][j] * inv);
-                if (i * 16 + 8 < D) dst[i * 16 + 8 + g] = Elem<DT>::from_float(o[i][nb][j + 2] * inv);
-              }
-              if (a.lse && g == 0)
-                a.lse[row * a.num_q_heads + head0 + head] =
-                    l[nb][j] == 0.f ? -CUDART_INF_F : (m[nb][j] - kShift) * CUDART_LN2_F + logf(l[nb][j]);
+              if (a.lse && g == 0 && head < gn) a.lse[row * a.num_q_heads + head0 + head] = lse_of(m[nb][j], l[nb][j]);
             }
+            // from head elements as rows to heads as rows: elements j * 8 + quad * 2 + {0, 1} of head g
+            uint16_t *dst = static_cast<uint16_t *>(a.out) + row * a.ldo + (head0 + nb * 8 + g) * D + quad * 2;
+#pragma unroll
+            for (int j = 0; j < DP / 8; ++j) {
+              const float *x = &o[j / 2][nb][(j & 1) * 2];
+              const uint32_t two = transpose8((uint32_t)Elem<DT>::from_float(x[0] * inv[0]) |
+                                              ((uint32_t)Elem<DT>::from_float(x[1] * inv[1]) << 16));
+              if (j * 8 < D && nb * 8 + g < gn) *reinterpret_cast<uint32_t *>(dst + j * 8) = two;
+            }
+          }
         } else {
           // with the first tile it is the warp's last piece, and the ring is idle
           const int piece = 2 * warp + (with_first ? 1 : 0);
@@ -611,7 +639,6 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     u.y = (uint32_t)Elem<DT>::from_float(f.z) | ((uint32_t)Elem<DT>::from_float(f.w) << 16);
     return u;
   };
-  auto lse_of = [&](float m, float l) { return l == 0.f ? -CUDART_INF_F : (m - kShift) * CUDART_LN2_F + logf(l); };
   auto warp_max = [&](float x) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
@@ -631,8 +658,8 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
   int heads = 0;
   int64_t head0 = 0;
   if (valid) {
-    const int64_t nt = sh.first[my_row + 1] - sh.first[my_row], begin = sh.first[my_row] * HC + my_hc * nt;
-    here = begin >= t0, done = here && begin + nt <= t1;
+    const int nt = sh.first[my_row + 1] - sh.first[my_row], begin = sh.first[my_row] * HC + my_hc * nt;
+    here = begin >= t0, done = here && begin + nt - empty <= t1;
     heads = heads_of(my_hc, head0);
   }
   const int64_t my_out = done ? ((int64_t)p.row0 + my_row) * a.ldo + head0 * D : here * (int64_t)partial_floats(DP);
@@ -697,9 +724,9 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
   for (int h = 0; h < 2; ++h) {
     if (open_row[h] < 0) continue;
     const int r = open_row[h];
-    const int64_t nt = sh.first[r + 1] - sh.first[r], begin = sh.first[r] * HC + open_hc[h] * nt;
+    const int nt = sh.first[r + 1] - sh.first[r], begin = sh.first[r] * HC + open_hc[h] * nt;
     c0[h] = cta_of(begin);
-    c1[h] = cta_of(begin + nt - 1);
+    c1[h] = cta_of(begin + nt - 1 - empty);
   }
   if (tid == 0) {
     __threadfence();  // the CTA's partial results (seen here by the barrier) before the count
@@ -798,6 +825,11 @@ cudaError_t dispatch(const AttnParams &p, int32_t *status, cudaStream_t stream) 
 
 }  // namespace
 
+bool kv_attention_fits(const mlora_kv_cache &c, const mlora_kv_attn &a) {
+  const int64_t chunks = (a.num_q_heads / c.num_kv_heads + kMaxGroup - 1) / kMaxGroup;
+  return ((int64_t)a.max_pages * c.page_tokens / kTile + 3) * c.num_kv_heads * chunks <= INT32_MAX;
+}
+
 int64_t kv_attention_workspace_bytes(int32_t head_dim) {
   const int dp = padded_dim(head_dim);
   return (int64_t)kCounterBytes + (int64_t)attn_ctas() * kPartialSlots * partial_floats(dp) * sizeof(float);
@@ -816,9 +848,13 @@ cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a,
   p.scale_log2 = a.scale * 1.44269504088896340736f;
   p.counters = static_cast<int32_t *>(a.workspace);
   p.partials = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kCounterBytes);
-  for (int32_t row0 = 0; row0 < a.num_rows; row0 += kRowsPerLaunch) {
+  // rows of a launch: few enough that its tiles are counted in 31 bits, whatever the lengths (with kNone's empty ones)
+  const int64_t row_tiles = ((int64_t)a.max_pages * c.page_tokens / kTile + 3) * c.num_kv_heads * p.chunks;
+  const int32_t step = (int32_t)std::min<int64_t>(kRowsPerLaunch, INT32_MAX / row_tiles);
+  if (step < 1) return cudaErrorInvalidValue;  // (refused before: kv_attention_fits)
+  for (int32_t row0 = 0; row0 < a.num_rows; row0 += step) {
     p.row0 = row0;
-    p.rows = min(kRowsPerLaunch, a.num_rows - row0);
+    p.rows = std::min(step, a.num_rows - row0);
     const cudaError_t e = c.dtype == MLORA_BF16 ? dispatch<MLORA_BF16>(p, status, stream)
                                                 : dispatch<MLORA_FP16>(p, status, stream);
     if (e != cudaSuccess) return e;

@@ -118,6 +118,7 @@ int lora_kv_attention(const mlora_kv_cache *cache, const mlora_kv_attn *a, int32
   if (a->num_rows < 0 || a->num_requests < 0 || a->window < 0) return MLORA_ERR_SHAPE;
   if (a->num_q_heads < 1 || a->num_q_heads % cache->num_kv_heads || !std::isfinite(a->scale)) return MLORA_ERR_SHAPE;
   TRY(check_table(a->max_pages, a->table_stride, cache->page_tokens));
+  if (!mlora::kv_attention_fits(*cache, *a)) return MLORA_ERR_SHAPE;
   if (a->num_rows == 0) return MLORA_OK;
   const int64_t width = (int64_t)a->num_q_heads * cache->head_dim;
   TRY(check_rows(a->q, a->ldq, width));

@@ -408,7 +408,8 @@ typedef struct {
   const int32_t *row_request;    /* [num_rows], or NULL: row i is request i */
   const int32_t *page_table;     /* [num_requests][table_stride] */
   int64_t table_stride;
-  int32_t num_requests, max_pages; /* max_pages * page_tokens < 2^31 */
+  int32_t num_requests, max_pages; /* max_pages * page_tokens < 2^31, times num_kv_heads (and every 16 query heads
+                                      of a group) below 2^34 */
   int32_t window;
   float scale;
   float *lse;                    /* [num_rows][num_q_heads], or NULL */

@@ -38,7 +38,9 @@ namespace mlora {
 
 namespace {
 
-constexpr int kTile = 16;            // tokens of a tile
+// Tokens of a tile: 16, and 32 where a head of at most 64 elements makes the tile's copies half as large
+// (64 rows of 8 x 64 elements: SIXTEEN us with 16, THIRTYTWO with 32).
+constexpr int tile_tokens(int dp) { return dp == 64 ? 32 : 16; }
 constexpr int kRowsPerLaunch = 1024;
 constexpr int kMinTiles = 2;         // a warp's share of a small call, so that few pieces have to be joined
 // A CTA's boundary inside a (row, head) of at most this many tiles moves to its nearer end, where the CTAs'
@@ -52,7 +54,7 @@ constexpr int kFewTiles = 16;
 constexpr float kSlack = 8.f;        // log2 of how far a weight may pass 1 before m moves
 
 constexpr int attn_warps(int dp) { return dp == 256 ? 4 : 8; }
-constexpr int attn_stages(int dp) { return dp == 64 ? 4 : 2; }
+constexpr int attn_stages(int) { return 2; }
 // Floats of a partial result: out [16][dp], then m [16] and l [16].
 constexpr int partial_floats(int dp) { return kMaxGroup * (dp + 2); }
 constexpr int kPartialSlots = 2;  // partial results of a CTA in the workspace
@@ -130,7 +132,8 @@ __device__ __forceinline__ void cp_async_wait() {
 
 // A tile's place, one per lane for 32 consecutive tiles of the list.
 struct Tile {
-  int64_t off;    // pages of whole tiles: its first token in the cache; else its request and first token
+  // pages of whole 16 tokens: where each 16 of its tokens start in the cache; else [0]: its request and first token
+  int64_t off[2];
   uint32_t seen;  // bit t: token t is seen
   uint32_t row;   // the row, with kFirst / kLast for the first / last tile of its (row, head), kNone for no tile
   int32_t hc;     // key-value head and chunk of its group
@@ -139,6 +142,7 @@ constexpr uint32_t kNone = 1u << 29, kFirst = 1u << 30, kLast = 1u << 31, kRowMa
 
 template <int DP, int NW, int NB>
 struct AttnSmem {
+  static constexpr int kTile = tile_tokens(DP);
   static constexpr int kStages = attn_stages(DP);
   static constexpr int kStageElems = 2 * kTile * DP;  // K, then V
   uint16_t ring[NW][kStages][kStageElems];  // a warp's tiles; after the last, its unfinished last piece
@@ -162,7 +166,8 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     kv_attention_kernel(const __grid_constant__ AttnParams p, int32_t *status) {
   constexpr int NW = attn_warps(DP), NT = NW * 32;
   using Smem = AttnSmem<DP, NW, NB>;
-  constexpr int S = Smem::kStages;
+  constexpr int S = Smem::kStages, kTile = Smem::kTile, H = kTile / 16;  // H halves of 16 tokens
+  constexpr uint32_t kAll = kTile == 32 ? ~0u : 0xFFFFu;
   constexpr int CH = DP / 8;    // 16-byte chunks of a token's head
   constexpr int GP = NB * 8;    // heads that a piece holds
   static_assert(GP * DP * 4 <= S * Smem::kStageElems * 2, "a piece fits in the ring");
@@ -307,8 +312,8 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       }
       const int pos = sh.pos[r], lo = a.window ? max(0, pos + 1 - a.window) : 0;
       const int t0 = (lo / kTile + tile) * kTile;
-      t.seen = 0xFFFFu;
-      if (t0 < lo) t.seen &= 0xFFFFu << (lo - t0);
+      t.seen = kAll;
+      if (t0 < lo) t.seen &= kAll << (lo - t0);
       if (pos - t0 < kTile - 1) t.seen &= (2u << (pos - t0)) - 1u;
       t.row = (uint32_t)r | (tile == 0 ? kFirst : 0u) | (tile == nt - 1 - empty ? kLast : 0u);
       const int64_t row = (int64_t)p.row0 + r;
@@ -319,17 +324,21 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         prefetch_l2(static_cast<const uint16_t *>(a.q) + row * a.ldq + head0 * D, (uint32_t)(heads * D * 2));
       }
       if constexpr (PAGED16) {
-        const int pg = div_by(p.page, t0);
-        const int id = a.page_table[(int64_t)req * a.table_stride + pg];
-        if (id >= 0 && id < p.c.num_pages) {
-          t.off = (int64_t)id * p.c.page_stride + (int64_t)(t0 - pg * p.page.d) * p.c.token_stride +
-                  (int64_t)(p.chunks == 1 ? t.hc : t.hc / p.chunks) * p.c.head_stride;
-        } else {
-          report(status, MLORA_STATUS_BAD_PAGE);
-          t.seen = 0;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          if (!((t.seen >> (16 * h)) & 0xFFFFu)) continue;
+          const int pg = div_by(p.page, t0 + 16 * h);
+          const int id = a.page_table[(int64_t)req * a.table_stride + pg];
+          if (id >= 0 && id < p.c.num_pages) {
+            t.off[h] = (int64_t)id * p.c.page_stride + (int64_t)(t0 + 16 * h - pg * p.page.d) * p.c.token_stride +
+                       (int64_t)(p.chunks == 1 ? t.hc : t.hc / p.chunks) * p.c.head_stride;
+          } else {
+            report(status, MLORA_STATUS_BAD_PAGE);
+            t.seen &= ~(0xFFFFu << (16 * h));
+          }
         }
       } else {
-        t.off = ((int64_t)req << 32) | (uint32_t)t0;
+        t.off[0] = ((int64_t)req << 32) | (uint32_t)t0;
       }
       return t;
     };
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     // the tile's own copies start (with the copies of a tile that is waited for before that).
     auto look_up = [&](int i) {
       const Tile &b = tile_at(i);
-      const int64_t at = __shfl_sync(~0u, b.off, i & 31);
+      const int64_t at = __shfl_sync(~0u, b.off[0], i & 31);
       const uint32_t range = __shfl_sync(~0u, b.seen, i & 31);
       const int t = (int)(uint32_t)at + lane;
       if (lane < kTile && ((range >> lane) & 1u))
@@ -356,17 +365,19 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       uint16_t *ks = sh.ring[warp][slot];
       if constexpr (PAGED16) {
         const Tile &b = tile_at(i);
-        const int64_t off = __shfl_sync(~0u, b.off, i & 31);
         const uint32_t seen = __shfl_sync(~0u, b.seen, i & 31);
         if (lane == 0) sh.seen[warp][slot] = seen;
         const bool none = (__shfl_sync(~0u, b.row, i & 31) & kNone) != 0;
-        if (copies && !none) {  // (a tile whose page is missing is filled with zeros)
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const int64_t off = __shfl_sync(~0u, b.off[h], i & 31);
+          if (!copies || none) continue;  // (a tile whose page is missing is filled with zeros)
           const int64_t at = off + (int64_t)lt * p.c.token_stride + lc * 8;
           const uint16_t *pk = p.k + at, *pv = p.v + at;
           const int64_t step = kStep * p.c.token_stride;
 #pragma unroll
-          for (int j = 0; j < kTile / kStep; ++j) {
-            const int t = j * kStep + lt;
+          for (int j = 0; j < 16 / kStep; ++j) {
+            const int t = 16 * h + j * kStep + lt;
             uint16_t *dst = ks + t * DP + ((lc ^ (t & 7)) * 8);
             const uint32_t bytes = (seen >> t) & 1u ? 16u : 0u;
             tc::cp_async16(dst, bytes ? pk : p.k, bytes);
@@ -377,9 +388,9 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       } else {
         const Tile &b = tile_at(i);
         const int hc = __shfl_sync(~0u, b.hc, i & 31);
-        const int t0 = (int)(uint32_t)__shfl_sync(~0u, b.off, i & 31) + (lane & 15);
-        const bool want = (__shfl_sync(~0u, b.seen, i & 31) >> (lane & 15)) & 1u;
-        const int id = want ? sh.page_id[warp][i % (2 * S)][lane & 15] : -1;
+        const int t0 = (int)(uint32_t)__shfl_sync(~0u, b.off[0], i & 31) + lane % kTile;
+        const bool want = (__shfl_sync(~0u, b.seen, i & 31) >> (lane % kTile)) & 1u;
+        const int id = want ? sh.page_id[warp][i % (2 * S)][lane % kTile] : -1;
         const bool good = id >= 0 && id < p.c.num_pages;
         if (want && !good) report(status, MLORA_STATUS_BAD_PAGE);
         if (lane < kTile)
@@ -387,7 +398,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
                                          (int64_t)(t0 - div_by(p.page, t0) * p.page.d) * p.c.token_stride +
                                          (int64_t)(p.chunks == 1 ? hc : hc / p.chunks) * p.c.head_stride
                                    : -1;
-        const uint32_t seen = __ballot_sync(~0u, good) & 0xFFFFu;  // (also orders at[] for the warp)
+        const uint32_t seen = __ballot_sync(~0u, good) & kAll;  // (also orders at[] for the warp)
         __syncwarp();
         if (lane == 0) sh.seen[warp][slot] = seen;
         if (copies) {
@@ -493,30 +504,35 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       const uint32_t seen = sh.seen[warp][slot];
       const uint32_t ks = smem_u32(sh.ring[warp][slot]), vs = ks + kTile * DP * 2;
 
-      float s[NB][4] = {}, s2[NB][4] = {};  // two chains of products
+      float s[H][NB][4] = {}, s2[H][NB][4] = {};  // two chains of products
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) {
-        uint32_t x[4];
-        ldmatrix4(x, ks + kt * DP * 2 + (((kk * 2 + kc) ^ (kt & 7)) << 4));
+      for (int kk = 0; kk < DP / 16; ++kk)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma<DT>(kk & 1 ? s2[nb] : s[nb], x, q[kk][nb][0], q[kk][nb][1]);
-      }
-      // s[nb][2 i + j]: token g + 8 i, head quad * 2 + j
-      const bool on[2] = {((seen >> g) & 1u) != 0, ((seen >> (g + 8)) & 1u) != 0};
+        for (int h = 0; h < H; ++h) {
+          uint32_t x[4];
+          ldmatrix4(x, ks + (16 * h + kt) * DP * 2 + (((kk * 2 + kc) ^ (kt & 7)) << 4));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma<DT>(kk & 1 ? s2[h][nb] : s[h][nb], x, q[kk][nb][0], q[kk][nb][1]);
+        }
+      // s[h][nb][2 i + j]: token 16 h + g + 8 i, head quad * 2 + j
       bool past = false;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[nb][j] = on[j >> 1] ? (s[nb][j] + s2[nb][j]) * p.scale_log2 : -CUDART_INF_F;
-          past |= s[nb][j] > m[nb][j & 1] + kSlack;
-        }
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bool on = ((seen >> (16 * h + g + 8 * (j >> 1))) & 1u) != 0;
+            s[h][nb][j] = on ? (s[h][nb][j] + s2[h][nb][j]) * p.scale_log2 : -CUDART_INF_F;
+            past |= s[h][nb][j] > m[nb][j & 1] + kSlack;
+          }
       if (__any_sync(~0u, past)) {  // m moves to the maximum
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float top = fmaxf(s[nb][j], s[nb][j + 2]);
+            float top = fmaxf(s[0][nb][j], s[0][nb][j + 2]);
+            if (H > 1) top = fmaxf(top, fmaxf(s[H - 1][nb][j], s[H - 1][nb][j + 2]));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
@@ -529,34 +545,38 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
             }
           }
       }
-      uint32_t hi[NB][2], lo[NB][2];  // P^T: tokens {0, 8} + quad * 2 + {0, 1}, head g
+      uint32_t hi[H][NB][2], lo[H][NB][2];  // P^T: tokens 16 h + {0, 8} + quad * 2 + {0, 1}, head g
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float base = m[nb][j & 1] == -CUDART_INF_F ? 0.f : m[nb][j & 1] - kShift;
-          w[j] = exp2_fast(s[nb][j] - base);
-          l[nb][j & 1] += w[j];
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t h, r;
-          split_pair<DT>(w[2 * i], w[2 * i + 1], h, r);
-          hi[nb][i] = transpose8(h);
-          lo[nb][i] = transpose8(r);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < DP / 16; ++j) {
-        uint32_t x[4];
-        ldmatrix4_t(x, vs + vt * DP * 2 + (((j * 2 + vc) ^ (vt & 7)) << 4));
+      for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          mma<DT>(o[j][nb], x, hi[nb][0], hi[nb][1]);
-          mma<DT>(o[j][nb], x, lo[nb][0], lo[nb][1]);
+          float w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float base = m[nb][j & 1] == -CUDART_INF_F ? 0.f : m[nb][j & 1] - kShift;
+            w[j] = exp2_fast(s[h][nb][j] - base);
+            l[nb][j & 1] += w[j];
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t big, left;
+            split_pair<DT>(w[2 * i], w[2 * i + 1], big, left);
+            hi[h][nb][i] = transpose8(big);
+            lo[h][nb][i] = transpose8(left);
+          }
         }
-      }
+#pragma unroll
+      for (int j = 0; j < DP / 16; ++j)
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          uint32_t x[4];
+          ldmatrix4_t(x, vs + (16 * h + vt) * DP * 2 + (((j * 2 + vc) ^ (vt & 7)) << 4));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma<DT>(o[j][nb], x, hi[h][nb][0], hi[h][nb][1]);
+            mma<DT>(o[j][nb], x, lo[h][nb][0], lo[h][nb][1]);
+          }
+        }
       __syncwarp();  // the slot may be filled again
       if (++slot == S) slot = 0;
 
@@ -810,7 +830,7 @@ cudaError_t launch(const AttnParams &p, int32_t *status, cudaStream_t stream) {
 
 template <int DT, int DP>
 cudaError_t dispatch(const AttnParams &p, int32_t *status, cudaStream_t stream) {
-  const bool whole = p.c.page_tokens % kTile == 0;
+  const bool whole = p.c.page_tokens % 16 == 0;
   if (p.group > 8) return whole ? launch<DT, DP, 2, true>(p, status, stream) : launch<DT, DP, 2, false>(p, status, stream);
   return whole ? launch<DT, DP, 1, true>(p, status, stream) : launch<DT, DP, 1, false>(p, status, stream);
 }
@@ -827,7 +847,7 @@ cudaError_t dispatch(const AttnParams &p, int32_t *status, cudaStream_t stream) 
 
 bool kv_attention_fits(const mlora_kv_cache &c, const mlora_kv_attn &a) {
   const int64_t chunks = (a.num_q_heads / c.num_kv_heads + kMaxGroup - 1) / kMaxGroup;
-  return ((int64_t)a.max_pages * c.page_tokens / kTile + 3) * c.num_kv_heads * chunks <= INT32_MAX;
+  return ((int64_t)a.max_pages * c.page_tokens / 16 + 3) * c.num_kv_heads * chunks <= INT32_MAX;
 }
 
 int64_t kv_attention_workspace_bytes(int32_t head_dim) {
@@ -849,7 +869,7 @@ cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a,
   p.counters = static_cast<int32_t *>(a.workspace);
   p.partials = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kCounterBytes);
   // rows of a launch: few enough that its tiles are counted in 31 bits, whatever the lengths (with kNone's empty ones)
-  const int64_t row_tiles = ((int64_t)a.max_pages * c.page_tokens / kTile + 3) * c.num_kv_heads * p.chunks;
+  const int64_t row_tiles = ((int64_t)a.max_pages * c.page_tokens / 16 + 3) * c.num_kv_heads * p.chunks;
   const int32_t step = (int32_t)std::min<int64_t>(kRowsPerLaunch, INT32_MAX / row_tiles);
   if (step < 1) return cudaErrorInvalidValue;  // (refused before: kv_attention_fits)
   for (int32_t row0 = 0; row0 < a.num_rows; row0 += step) {

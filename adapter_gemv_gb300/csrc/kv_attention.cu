@@ -39,7 +39,7 @@ namespace mlora {
 namespace {
 
 // Tokens of a tile: 16, and 32 where a head of at most 64 elements makes the tile's copies half as large
-// (64 rows of 8 x 64 elements: SIXTEEN us with 16, THIRTYTWO with 32).
+// (64 rows of 8 x 64 elements: 41.9 us with 16, 39.8 with 32).
 constexpr int tile_tokens(int dp) { return dp == 64 ? 32 : 16; }
 constexpr int kRowsPerLaunch = 1024;
 constexpr int kMinTiles = 2;         // a warp's share of a small call, so that few pieces have to be joined

@@ -4,21 +4,23 @@
 // mask bit against a handful of flops, so bound by memory for a batch and by latency for a row.
 //
 // A CTA takes a slice of one row's vocabulary and streams it through: temperature and mask, which need no
-// table. Few of its tokens are in the request's history or bias list; a bit per token says which, and they
-// are worked out behind the stream, a thread a token, from the logits as they came, over what the stream has
-// written there (where out is logits the stream leaves them alone: 69 us instead of 64 below, as vectors with such
-// a token go out in parts). So the stream needs few registers and small tables, and four CTAs share an SM:
-// while one waits for its row's lengths, its history or its counts, the others stream.
+// table. Few of its tokens are in the request's history or bias list. They are worked out behind the
+// stream, a thread a token, from the logits as they came, over what the stream has written there. (Where out is
+// logits, the bits below are made before the stream, and it leaves those tokens alone.) So the stream needs
+// few registers and waits for nothing but the row's parameters, the tables are small, and four CTAs share an
+// SM: while one waits for its history or its counts, the others stream.
+// A bit per token says which are in the history or the list.
 // The touched tokens are numbered by their place among the bits set (a prefix sum over the words), and have
 // their count (occurrences past the prompt, whole-number atomics: the order does not matter; bit 31 for a
 // token of the prompt) and bias (the entry's number + 1, then its value, as one 64-bit maximum: of several
 // with one id the last wins) in arrays by that number; more than kPlaces of them, of a long history, take
 // several turns. Each CTA of a row reads the whole history: at most some 16 KB, from L2 after the first.
-// Measured at 256 x 128001 fp32 with histories of 512 to 4096 tokens, lists of 300 and half the rows masked: 64 us,
-// 4.1 TB/s (43 us, 6.1 TB/s, without history, list and mask); it is the instructions around the tables, issued
-// in two of three cycles. Also tried there: a table entry for every token of the slice, its logits held in
-// registers until the counts were there, 88 us; the touched tokens adjusted in the stream, with the counts before
-// it, 75 to 82; a CTA's share as one long stretch, 76; a division replaced by a corrected product, no gain.
+// Measured at 256 x 128001 fp32 with histories of 512 to 4096 tokens, lists of 300 and half the rows masked: 61 us,
+// 4.3 TB/s (43 us, 6.1 TB/s, without history, list and mask). What is left is the touched tokens' chain: bits
+// 4 us, numbers 1, counts 8, their logits 4. Also tried there: a table entry for every token of the slice,
+// its logits held in registers until the counts were there, 88 us; the touched tokens adjusted in the stream, with
+// the counts before it, 75 to 82; a CTA's share as one long stretch, 76; a list of the slice's tokens in
+// shared memory instead of reading the history twice, 69; more CTAs an SM with fewer registers, 64 to 76.
 //
 // Rows of an odd vocabulary start at any multiple of the element: a slice is cut where 16-byte
 // vectors are aligned in memory, counted from the aligned address before the row's start.
@@ -58,8 +60,9 @@ struct Vec<MLORA_FP32> {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroup = 4;    // vectors of a thread that are loaded together
+constexpr int kEarlyBias = 2;  // and entries of the list
 constexpr int kEarly = 4;    // tokens of the history that a thread loads ahead
-constexpr int kPlaces = 1024;
+constexpr int kPlaces = 512;
 constexpr uint32_t kInPrompt = 0x80000000u;
 
 template <int SLICE>
@@ -146,8 +149,14 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
 
   // ---- which tokens of the slice are in the history or the list --------------------------------------
   const int listed = bias1 - bias0;
-  const int early_bias = tid < listed ? p.bias_token[bias0 + tid] : 0;
-  const float early_value = tid < listed ? p.bias_value[bias0 + tid] : 0.f;
+  int early_bias[kEarlyBias];
+  float early_value[kEarlyBias];
+#pragma unroll
+  for (int k = 0; k < kEarlyBias; ++k) {
+    const int i = k * kThreads + tid;
+    early_bias[k] = i < listed ? p.bias_token[bias0 + i] : 0;
+    early_value[k] = i < listed ? p.bias_value[bias0 + i] : 0.f;
+  }
   const bool touched = total > 0 || listed > 0;
   const uint32_t *bits = grammar >= 0 ? p.mask + grammar * p.mask_stride : nullptr;
   const int word0 = first >> 5, last_word = (p.vocab - 1) >> 5;  // (first may be below 0)
@@ -162,8 +171,10 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     for (int i = kEarly * kThreads + tid; i < total; i += kThreads) f(i, text[i]);
   };
   auto each_entry = [&](auto f) {  // of the list, with its value
-    if (tid < listed) f(tid, early_bias, early_value);
-    for (int i = kThreads + tid; i < listed; i += kThreads) f(i, p.bias_token[bias0 + i], p.bias_value[bias0 + i]);
+#pragma unroll
+    for (int k = 0; k < kEarlyBias; ++k)
+      if (k * kThreads + tid < listed) f(k * kThreads + tid, early_bias[k], early_value[k]);
+    for (int i = kEarlyBias * kThreads + tid; i < listed; i += kThreads) f(i, p.bias_token[bias0 + i], p.bias_value[bias0 + i]);
   };
   int kept = 0;  // how many tokens
   // counts and biases of the tokens numbered from .. from + kPlaces - 1
@@ -173,7 +184,9 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
   };
   auto count_from = [&](int from) {
     const uint32_t n = (uint32_t)min(kPlaces, kept - from);
-    for (int j = tid; j < (int)n; j += kThreads) sh.count[j] = 0, sh.bias[j] = 0;
+    if (from) {  // (for the first turn they were cleared with the bits)
+      for (int j = tid; j < kPlaces; j += kThreads) sh.count[j] = 0, sh.bias[j] = 0;
+    }
     __syncthreads();
     each_token([&](int i, int t) {
       if (!inside(t)) return;
@@ -199,19 +212,21 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     const unsigned long long b = sh.bias[j];
     return b ? f + __uint_as_float((uint32_t)b) : f;
   };
-  if (touched) {
+  auto mark_all = [&]() {
     for (int i = tid; i < Smem::kWords; i += kThreads) sh.hit[i] = 0;
+    for (int j = tid; j < kPlaces; j += kThreads) sh.count[j] = 0, sh.bias[j] = 0;
     __syncthreads();
     int wrong = 0;
-    auto mark = [&](int, int t) {
+    auto mark = [&](int t) {
       if (slice == 0 && (uint32_t)t >= (uint32_t)p.vocab) wrong = MLORA_STATUS_BAD_TOKEN;
       if (inside(t)) atomicOr(&sh.hit[(t - first) >> 5], 1u << ((t - first) & 31));
     };
-    each_token(mark);
-    each_entry([&](int i, int t, float) { mark(i, t); });
+    each_token([&](int, int t) { mark(t); });
+    each_entry([&](int, int t, float) { mark(t); });
     if (wrong) report(status, wrong);
-  }
-  if (touched || bits) __syncthreads();
+  };
+  if (touched && in_place) mark_all();
+  if ((touched && in_place) || bits) __syncthreads();
 
   // ---- the stream -------------------------------------------------------------------------------------
 #pragma unroll 1
@@ -247,6 +262,8 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     }
   }
   if (!touched) return;
+  if (!in_place) mark_all();
+  __syncthreads();  // (also: what the stream has written comes before what follows)
 
   // ---- the touched tokens ------------------------------------------------------------------------------------
   {

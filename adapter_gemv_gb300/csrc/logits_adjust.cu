@@ -321,10 +321,18 @@ cudaError_t launch(const mlora_logits &a, int32_t *status, cudaStream_t stream) 
 
 template <int DT>
 cudaError_t dispatch(const mlora_logits &a, int32_t *status, cudaStream_t stream) {
-  // Slices of 16384 tokens; where that gives the SMs less than one each to do (at 4096 tokens an SM), slices of
-  // one vector a thread: a row of 32000 takes 3.4 us so, and 5.3 in slices of 4096.
-  if ((int64_t)a.num_rows * a.vocab < (int64_t)sm_count() * 4096) return launch<DT, 0>(a, status, stream);
-  return launch<DT, DT == MLORA_FP32 ? 4 : 2>(a, status, stream);
+  // The longer the slices, the fewer times a row's history is read and counted; the shorter, the more SMs
+  // work. By the CTAs that slices of kGroup vectors a thread would give (fp32: 4096 tokens), an SM's share
+  // of them; measured (us) with slices of 1, 4, 8 and 16 vectors a thread:
+  //   4 x 38319 (40 CTAs): 4.2  5.8  7.5  14.3     24 x 47632 (288): 8.8  6.3  7.5  10.8
+  //   64 x 32000 (512): 14.3  7.5  7.9  10.9       32 x 128001 (1024): 24.6  12.8  11.9  13.8
+  //   64 x 128001 (2048): 48.7  23.5  20.4  18.6   256 x 32000 (2048): 54.3  24.5  20.3  18.3
+  constexpr int kPiece = kThreads * kGroup * Vec<DT>::N;
+  const int64_t ctas = (int64_t)a.num_rows * (((int64_t)a.vocab + kPiece - 1) / kPiece), sms = sm_count();
+  if (ctas < sms) return launch<DT, 0>(a, status, stream);
+  if (ctas < 5 * sms) return launch<DT, 1>(a, status, stream);
+  if (ctas < 10 * sms) return launch<DT, 2>(a, status, stream);
+  return launch<DT, 4>(a, status, stream);
 }
 
 }  // namespace

@@ -124,12 +124,12 @@ class KvBatch:
         s.row_request, s.position = self.row_request.data_ptr(), self.position.data_ptr()
         s.cache_slot, s.row_slot = self.cache_slot.data_ptr(), self.row_slot.data_ptr()
         s.seg_offsets, s.seg_slot = self.seg_offsets.data_ptr(), self.seg_slot.data_ptr()
-        self.ref = ctypes.pointer(s)
+        self.ref, self.fn = ctypes.pointer(s), lib().lora_kv_layout
 
 
 def lora_kv_layout(batch: KvBatch, status=None, stream=None) -> None:
     """Pages and row places of a step from its requests' lengths (writes the batch's arrays)."""
-    _check(lib().lora_kv_layout(batch.ref, _i32(status, "status"), _stream(stream)))
+    _check(batch.fn(batch.ref, 0 if status is None else _i32(status, "status"), _stream(stream)))
 
 
 class KvCache:

@@ -290,7 +290,8 @@ MLORA_API int lora_sgmv_sequence(const mlora_group *groups, int32_t num_groups, 
  *     arrays; a row that stands for nothing has -1 as its request, position and cache slot, and no
  *     call reads or writes anything for it but where said.
  *   - Every kernel waits for the work before it in the stream before it reads or writes any memory,
- *     whether or not it was launched programmatically. */
+ *     whether or not it was launched programmatically. lora_kv_layout writes the segments that the adapters' calls
+ *     read before such a wait: the first of them after it is launched without MLORA_LAUNCH_PROGRAMMATIC. */
 
 #define MLORA_KV_MAX_REQUESTS 8192
 #define MLORA_KV_MAX_HEAD_DIM 256

@@ -8,12 +8,14 @@
 // most 16 heads a group the matrix instructions are nearly idle and everything is about keeping
 // loads in flight. Therefore:
 //   * A warp works alone. It streams tiles of 16 tokens of one key-value head through a ring of its own
-//     in shared memory (16-byte cp.async, three tiles of 8 KB at 128 elements a head: some 130 KB on
+//     in shared memory (16-byte cp.async, two tiles of 8 KB at 128 elements a head: some 130 KB on
 //     their way per SM), with no barrier between warps in the loop.
 //   * The unit of work is a tile, not a request: the tiles of all rows and key-value heads form one
 //     list, cut evenly over the SMs and over their warps, so the lengths do not have to match anything and one
 //     long request fills the GPU as well as many short ones. A warp goes from one (row, head) to the
 //     next without draining its ring. Every 32 tiles its lanes work out 32 tiles' places at once.
+//   * Consecutive rows of one request (drafted tokens, a prompt) stand beside each other in a tile's 16 columns, as
+//     many as the group leaves room for, each with a mask of its own (kPackItems has the rule and the figures).
 //   * A (row, head) cut between warps is joined in two steps, in a fixed order: the warps of a CTA, in
 //     shared memory, then the CTAs, by the one that finishes last (a counter that it returns to zero).
 // What a warp does between two tiles has to stay below the time its share of the bandwidth gives it
@@ -51,6 +53,12 @@ constexpr int kMaxGroup = 16;        // query heads of a work item
 // and ending one costs, about a tile's products (0.5 us), counts beside the tiles then, not in a call that
 // waits for memory.
 constexpr int kFewTiles = 16;
+// Rows of one request share a tile's columns (a row takes `group` of 16) from this many (row, key-value head)s on, about
+// seven for each SM. It reads a tile once for all of them, at twice the products and longer joins. Measured on 8 heads of
+// 128, group 4, without and with: 32 requests x 4 rows, 500 to 1500 tokens 55.3 and 39.6 us; 64 x 2 69.9 and 52.7;
+// a prompt of 1024 tokens 346 and 179. Below: 8 requests x 4 rows 22.7 and 27.4, 1 x 4 rows of 300 tokens 8.7 and 14.8
+// (but 8 x 4 rows of 2000 to 4000 tokens 45.4 and 35.6: the lengths are not known to the host).
+constexpr int kPackItems = 1024;
 constexpr float kSlack = 8.f;        // log2 of how far a weight may pass 1 before m moves
 
 constexpr int attn_warps(int dp) { return dp == 256 ? 4 : 8; }
@@ -67,6 +75,8 @@ struct AttnParams {
   FastDiv page;
   int32_t row0, rows;     // this launch's rows
   int32_t group, chunks;  // query heads of a key-value head, in chunks of at most 16
+  int32_t pack;           // rows of one request that share a tile's columns, at most
+  FastDiv by_group;
   float scale_log2;       // scale * log2(e)
   int32_t *counters;      // [CTAs], zero between calls
   float *partials;        // [CTAs][kPartialSlots][partial_floats]
@@ -140,7 +150,7 @@ struct Tile {
 };
 constexpr uint32_t kNone = 1u << 29, kFirst = 1u << 30, kLast = 1u << 31, kRowMask = kNone - 1;
 
-template <int DP, int NW, int NB>
+template <int DP, int NW, int NB, bool PACK>
 struct AttnSmem {
   static constexpr int kTile = tile_tokens(DP);
   static constexpr int kStages = attn_stages(DP);
@@ -149,6 +159,9 @@ struct AttnSmem {
   float head[NW][NB * 8][DP];               // its unfinished first piece
   int32_t first[kRowsPerLaunch + 1];        // tiles (of one head) before a row
   int32_t pos[kRowsPerLaunch];              // last token seen; -1: none, -2: a bad row
+  // PACK, of a pack's first row: the first and the last token that its rows see, and their number (0: not a first row)
+  int32_t low[PACK ? kRowsPerLaunch : 1], high[PACK ? kRowsPerLaunch : 1];
+  uint8_t rows[PACK ? kRowsPerLaunch : 1];
   int32_t req[kRowsPerLaunch];              // the row's request
   uint32_t seen[NW][kStages];               // bit t: token t of the tile is seen
   int32_t warp_sum[NW], warp_rows[NW];
@@ -160,12 +173,13 @@ struct AttnSmem {
   int32_t last[2];
 };
 
-// PAGED16: a page holds whole tiles. NB: blocks of 8 heads of a group's chunk.
-template <int DT, int DP, int NB, bool PAGED16>
+// PAGED16: a page holds whole tiles. NB: blocks of 8 columns (heads of a group's chunk). PACK: rows of one request share
+// them.
+template <int DT, int DP, int NB, bool PAGED16, bool PACK>
 __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     kv_attention_kernel(const __grid_constant__ AttnParams p, int32_t *status) {
   constexpr int NW = attn_warps(DP), NT = NW * 32;
-  using Smem = AttnSmem<DP, NW, NB>;
+  using Smem = AttnSmem<DP, NW, NB, PACK>;
   constexpr int S = Smem::kStages, kTile = Smem::kTile, H = kTile / 16;  // H halves of 16 tokens
   constexpr uint32_t kAll = kTile == 32 ? ~0u : 0xFFFFu;
   constexpr int CH = DP / 8;    // 16-byte chunks of a token's head
@@ -183,26 +197,61 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
   // ---- the list of tiles: exclusive sums of the rows' tile counts ------------------------------
   const int R = p.rows;
   int empty;  // 1: an empty tile behind every (row, head)
+  auto low_of = [&](int pos) { return a.window ? max(0, pos + 1 - a.window) : 0; };  // the first token that is seen
   {
-    const int each = (R + NT - 1) / NT;
+    const int each = (R + NT - 1) / NT, r0 = min(tid * each, R), r1 = min(r0 + each, R);
     int sum = 0, some = 0, bad = 0;  // tiles; rows that have any
-    for (int i = 0; i < each; ++i) {
-      const int r = tid * each + i;
-      if (r >= R) break;
+    for (int r = r0; r < r1; ++r) {
       const int64_t row = (int64_t)p.row0 + r;
       int pos = a.position[row], n = 0;
       const int req = a.row_request ? a.row_request[row] : (int)row;
       if (pos < -1 || pos >= (int64_t)a.max_pages * p.page.d) bad |= MLORA_STATUS_BAD_LENGTH, pos = -2;
       else if (pos >= 0 && (req < 0 || req >= a.num_requests)) bad |= MLORA_STATUS_BAD_REQUEST, pos = -2;
-      if (pos >= 0) {
-        const int lo = a.window ? max(0, pos + 1 - a.window) : 0;
-        n = pos / kTile - lo / kTile + 1;
-      }
       sh.pos[r] = pos;
       sh.req[r] = req;
+      if (PACK) continue;
+      if (pos >= 0) n = pos / kTile - low_of(pos) / kTile + 1;
       sh.first[r] = n;
       sum += n;
       some += n > 0;
+    }
+    if (PACK) {
+      // Rows that follow each other, of one request, whose tokens overlap or touch, are a run; its rows from the
+      // first, p.pack at a time, are packs. A pack's first row stands for it; the others have no tiles.
+      auto starts_run = [&](int r) {
+        return r == 0 || sh.pos[r] < 0 || sh.pos[r - 1] < 0 || sh.req[r] != sh.req[r - 1] ||
+               low_of(sh.pos[r]) > sh.pos[r - 1] + 1 || sh.pos[r] + 1 < low_of(sh.pos[r - 1]);
+      };
+      __syncthreads();
+      int last = -1;
+      for (int r = r0; r < r1; ++r)
+        if (starts_run(r)) last = r;
+      int upto = last;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(~0u, upto, d);
+        if (lane >= d) upto = max(upto, x);
+      }
+      if (lane == 31) sh.warp_sum[warp] = upto;
+      int run = __shfl_up_sync(~0u, upto, 1);
+      if (lane == 0) run = -1;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) run = max(run, sh.warp_sum[w]);
+      for (int r = r0; r < r1; ++r) {
+        if (starts_run(r)) run = r;
+        int lo = low_of(sh.pos[r]), hi = sh.pos[r], count = 0, n = 0;
+        if ((r - run) % p.pack == 0) {
+          for (count = 1; count < p.pack && r + count < R && !starts_run(r + count); ++count) {
+            lo = min(lo, low_of(sh.pos[r + count]));
+            hi = max(hi, sh.pos[r + count]);
+          }
+          n = hi >= 0 ? hi / kTile - lo / kTile + 1 : 0;
+        }
+        sh.low[r] = lo, sh.high[r] = hi, sh.rows[r] = count, sh.first[r] = n;
+        sum += n;
+        some += n > 0;
+      }
+      __syncthreads();
     }
     int incl = sum, rows = some;
 #pragma unroll
@@ -221,9 +270,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     }
     empty = (int64_t)all * HC <= (int64_t)gridDim.x * NW * kFewTiles ? 1 : 0;
     at += empty * before;
-    for (int i = 0; i < each; ++i) {
-      const int r = tid * each + i;
-      if (r >= R) break;
+    for (int r = r0; r < r1; ++r) {
       const int n = sh.first[r];
       sh.first[r] = at;
       at += n ? n + empty : 0;
@@ -280,12 +327,16 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
   const int w0 = t0 + warp * each + min(warp, over);
   const int n = warp < nw ? each + (warp < over ? 1 : 0) : 0;
 
-  // the query heads of an item: the first one's number, and how many
-  auto heads_of = [&](int hc, int64_t &head0) {
+  // The columns of an item (row r, head and chunk hc): the query heads of its chunk, or those of its pack's rows. Head
+  // head0 of row r is the first; column c is head in(c) behind it, of row below(c) behind r.
+  auto columns = [&](int r, int hc, int64_t &head0) {
     const int hk = p.chunks == 1 ? hc : hc / p.chunks, g0 = p.chunks == 1 ? 0 : (hc - hk * p.chunks) * kMaxGroup;
     head0 = (int64_t)hk * p.group + g0;
+    if (PACK) return sh.rows[r] * p.group;  // (one chunk)
     return min(p.group - g0, kMaxGroup);
   };
+  auto below = [&](int c) { return PACK ? div_by(p.by_group, c) : 0; };
+  auto in = [&](int c) { return c - below(c) * p.group; };
   auto lse_of = [&](float m, float l) { return l == 0.f ? -CUDART_INF_F : (m - kShift) * CUDART_LN2_F + logf(l); };
   float *const partials = p.partials + (int64_t)blockIdx.x * kPartialSlots * partial_floats(DP);
   // chunks past the head's end are never copied: zero for good
@@ -310,7 +361,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         t.row = kNone;
         return t;
       }
-      const int pos = sh.pos[r], lo = a.window ? max(0, pos + 1 - a.window) : 0;
+      const int pos = PACK ? sh.high[r] : sh.pos[r], lo = PACK ? sh.low[r] : low_of(pos);
       const int t0 = (lo / kTile + tile) * kTile;
       t.seen = kAll;
       if (t0 < lo) t.seen &= kAll << (lo - t0);
@@ -320,8 +371,9 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       const int req = sh.req[r];
       if (tile == 0 || i == 0) {  // q of the (row, head), into L2
         int64_t head0;
-        const int heads = heads_of(t.hc, head0);
-        prefetch_l2(static_cast<const uint16_t *>(a.q) + row * a.ldq + head0 * D, (uint32_t)(heads * D * 2));
+        const int heads = min(columns(r, t.hc, head0), p.group);
+        for (int k = 0; k < (PACK ? sh.rows[r] : 1); ++k)
+          prefetch_l2(static_cast<const uint16_t *>(a.q) + (row + k) * a.ldq + head0 * D, (uint32_t)(heads * D * 2));
       }
       if constexpr (PAGED16) {
 #pragma unroll
@@ -435,25 +487,30 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     uint32_t ahead[DP / 16][NB][2];  // the next (row, head)'s, on its way while the last tile before it is computed
     auto load_q = [&](int i) {
       const Tile &b = tile_at(i);
-      const int64_t r = (int64_t)p.row0 + (int)(__shfl_sync(~0u, b.row, i & 31) & kRowMask);
+      const int r = (int)(__shfl_sync(~0u, b.row, i & 31) & kRowMask);
       int64_t h0;
-      const int heads = heads_of(__shfl_sync(~0u, b.hc, i & 31), h0);
-      const uint16_t *qr = static_cast<const uint16_t *>(a.q) + r * a.ldq + h0 * D;
+      const int cols = columns(r, __shfl_sync(~0u, b.hc, i & 31), h0);
+      const uint16_t *qr[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int c = min(nb * 8 + g, cols - 1);
+        qr[nb] = static_cast<const uint16_t *>(a.q) + ((int64_t)p.row0 + r + below(c)) * a.ldq + (h0 + in(c)) * D;
+      }
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int head = nb * 8 + g, d = kk * 16 + j * 8 + quad * 2;
-            ahead[kk][nb][j] =
-                head < heads && d < D ? *reinterpret_cast<const uint32_t *>(qr + (int64_t)head * D + d) : 0u;
+            const int d = kk * 16 + j * 8 + quad * 2;
+            ahead[kk][nb][j] = nb * 8 + g < cols && d < D ? *reinterpret_cast<const uint32_t *>(qr[nb] + d) : 0u;
           }
     };
     constexpr bool kAhead = DP * NB < 512;  // (no registers left for it at 16 heads of 256)
     float o[DP / 16][NB][4];     // O^T: elements j * 16 + g (0, 1) and + 8 (2, 3), heads quad * 2 + {0, 1}
     float m[NB][2], l[NB][2];    // of heads quad * 2 + {0, 1}; l: of this lane's tokens
     bool start = true, with_first = false;
+    int token = 0, sees[NB][2];  // packed rows: the tile's token g, and the last token that a column sees
     int row_in = 0, hc = 0, gn = 0;
     int64_t row = 0, head0 = 0;
     // lane's row and chunk in ldmatrix: K (token, plain) and V (token, transposed)
@@ -477,7 +534,15 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         hc = __shfl_sync(~0u, cur.hc, it & 31);
         with_first = (meta & kFirst) != 0;
         row = (int64_t)p.row0 + row_in;
-        gn = heads_of(hc, head0);
+        gn = columns(row_in, hc, head0);
+        if (PACK) {
+          const int nt = sh.first[row_in + 1] - sh.first[row_in];
+          token = (sh.low[row_in] / kTile + (w0 + it - sh.first[row_in] * HC - hc * nt)) * kTile + g;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) sees[nb][j] = sh.pos[row_in + below(min(nb * 8 + quad * 2 + j, gn - 1))];
+        }
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk)
 #pragma unroll
@@ -522,10 +587,15 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const bool on = ((seen >> (16 * h + g + 8 * (j >> 1))) & 1u) != 0;
+            bool on = ((seen >> (16 * h + g + 8 * (j >> 1))) & 1u) != 0;
+            if (PACK) {
+              const int t = token + 16 * h + 8 * (j >> 1), last = sees[nb][j & 1];
+              on = on && t <= last && t >= low_of(last);
+            }
             s[h][nb][j] = on ? (s[h][nb][j] + s2[h][nb][j]) * p.scale_log2 : -CUDART_INF_F;
             past |= s[h][nb][j] > m[nb][j & 1] + kSlack;
           }
+      token += kTile;
       if (__any_sync(~0u, past)) {  // m moves to the maximum
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -597,11 +667,13 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               inv[j] = l[nb][j] == 0.f ? 0.f : 1.f / l[nb][j];
-              const int head = nb * 8 + quad * 2 + j;
-              if (a.lse && g == 0 && head < gn) a.lse[row * a.num_q_heads + head0 + head] = lse_of(m[nb][j], l[nb][j]);
+              const int c = nb * 8 + quad * 2 + j;
+              if (a.lse && g == 0 && c < gn)
+                a.lse[(row + below(c)) * a.num_q_heads + head0 + in(c)] = lse_of(m[nb][j], l[nb][j]);
             }
             // from head elements as rows to heads as rows: elements j * 8 + quad * 2 + {0, 1} of head g
-            uint16_t *dst = static_cast<uint16_t *>(a.out) + row * a.ldo + (head0 + nb * 8 + g) * D + quad * 2;
+            const int c = min(nb * 8 + g, gn - 1);
+            uint16_t *dst = static_cast<uint16_t *>(a.out) + (row + below(c)) * a.ldo + (head0 + in(c)) * D + quad * 2;
 #pragma unroll
             for (int j = 0; j < DP / 8; ++j) {
               const float *x = &o[j / 2][nb][(j & 1) * 2];
@@ -680,10 +752,10 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
   if (valid) {
     const int nt = sh.first[my_row + 1] - sh.first[my_row], begin = sh.first[my_row] * HC + my_hc * nt;
     here = begin >= t0, done = here && begin + nt - empty <= t1;
-    heads = heads_of(my_hc, head0);
+    heads = columns(my_row, my_hc, head0);
   }
   const int64_t my_out = done ? ((int64_t)p.row0 + my_row) * a.ldo + head0 * D : here * (int64_t)partial_floats(DP);
-  for (int head = warp; head < GP; head += NW) {
+  for (int head = warp; head < GP; head += NW) {  // (a column)
     float top = -CUDART_INF_F, sum = 0.f, w = 0.f;
     if (head < heads) {
       for (uint32_t left = run; left; left &= left - 1) top = fmaxf(top, sh.m[__ffs(left) - 1][head]);
@@ -699,7 +771,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
           float *to = partials + my_out + kMaxGroup * DP + head;
           to[0] = top, to[16] = sum;
         } else if (a.lse) {
-          a.lse[((int64_t)p.row0 + my_row) * a.num_q_heads + head0 + head] = lse_of(top, sum);
+          a.lse[((int64_t)p.row0 + my_row + below(head)) * a.num_q_heads + head0 + in(head)] = lse_of(top, sum);
         }
       }
     }
@@ -724,7 +796,9 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         }
         if (i >= DP / 4) continue;
         if (!(flags & 1)) reinterpret_cast<float4 *>(partials + out)[head * (DP / 4) + i] = acc;
-        else if (i * 4 < D) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + out + head * D + i * 4) = pack4(acc);
+        else if (i * 4 < D)
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + out + below(head) * a.ldo + in(head) * D + i * 4) =
+              pack4(acc);
       }
     }
   }
@@ -768,7 +842,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       return p.partials + ((int64_t)(c0[h] + k) * kPartialSlots + (k == 0 ? 1 : 0)) * partial_floats(DP);
     };
     int64_t h0;
-    const int hn = heads_of(open_hc[h], h0);
+    const int hn = columns(open_row[h], open_hc[h], h0);
     const int64_t row = (int64_t)p.row0 + open_row[h];
     for (int head = warp; head < hn; head += NW) {
       // 32 partial results at a time, lane j at the j-th; their m and l, and the first ones' elements, at once
@@ -806,9 +880,10 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
         acc[i].x *= inv, acc[i].y *= inv, acc[i].z *= inv, acc[i].w *= inv;
         const int j = i * 32 + lane;
         if (j < DP / 4 && j * 4 < D)
-          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * a.ldo + (h0 + head) * D + j * 4) = pack4(acc[i]);
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + (row + below(head)) * a.ldo + (h0 + in(head)) * D +
+                                     j * 4) = pack4(acc[i]);
       }
-      if (a.lse && lane == 0) a.lse[row * a.num_q_heads + h0 + head] = lse_of(top, sum);
+      if (a.lse && lane == 0) a.lse[(row + below(head)) * a.num_q_heads + h0 + in(head)] = lse_of(top, sum);
     }
   }
 }
@@ -816,23 +891,28 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
 constexpr size_t kCounterBytes = 4096;
 int attn_ctas() { return min(sm_count(), (int)(kCounterBytes / sizeof(int32_t))); }  // one per SM
 
-template <int DT, int DP, int NB, bool PAGED16>
+template <int DT, int DP, int NB, bool PAGED16, bool PACK>
 cudaError_t launch(const AttnParams &p, int32_t *status, cudaStream_t stream) {
-  using Smem = AttnSmem<DP, attn_warps(DP), NB>;
+  using Smem = AttnSmem<DP, attn_warps(DP), NB, PACK>;
   static_assert(sizeof(Smem) <= 227 * 1024, "fits in shared memory");
-  cudaError_t e = raise_smem<kv_attention_kernel<DT, DP, NB, PAGED16>>((int)sizeof(Smem));
+  cudaError_t e = raise_smem<kv_attention_kernel<DT, DP, NB, PAGED16, PACK>>((int)sizeof(Smem));
   if (e != cudaSuccess) return e;
-  e = launch_waiting(kv_attention_kernel<DT, DP, NB, PAGED16>, dim3(attn_ctas()), dim3(attn_warps(DP) * 32), sizeof(Smem), 1,
-                     stream, p, status);
+  e = launch_waiting(kv_attention_kernel<DT, DP, NB, PAGED16, PACK>, dim3(attn_ctas()), dim3(attn_warps(DP) * 32),
+                     sizeof(Smem), 1, stream, p, status);
   if (e == cudaSuccess) api_count_launch();
   return e;
 }
 
+template <int DT, int DP, bool PAGED16>
+cudaError_t dispatch_columns(const AttnParams &p, int32_t *status, cudaStream_t stream) {
+  if (p.pack > 1) return launch<DT, DP, 2, PAGED16, true>(p, status, stream);
+  if (p.group > 8) return launch<DT, DP, 2, PAGED16, false>(p, status, stream);
+  return launch<DT, DP, 1, PAGED16, false>(p, status, stream);
+}
 template <int DT, int DP>
 cudaError_t dispatch(const AttnParams &p, int32_t *status, cudaStream_t stream) {
-  const bool whole = p.c.page_tokens % 16 == 0;
-  if (p.group > 8) return whole ? launch<DT, DP, 2, true>(p, status, stream) : launch<DT, DP, 2, false>(p, status, stream);
-  return whole ? launch<DT, DP, 1, true>(p, status, stream) : launch<DT, DP, 1, false>(p, status, stream);
+  return p.c.page_tokens % 16 == 0 ? dispatch_columns<DT, DP, true>(p, status, stream)
+                                   : dispatch_columns<DT, DP, false>(p, status, stream);
 }
 template <int DT>
 cudaError_t dispatch(const AttnParams &p, int32_t *status, cudaStream_t stream) {
@@ -865,6 +945,10 @@ cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a,
   p.page = fast_div(c.page_tokens);
   p.group = a.num_q_heads / c.num_kv_heads;
   p.chunks = (p.group + kMaxGroup - 1) / kMaxGroup;
+  // A drafted continuation, a prompt: as many of a request's rows as have room beside each other share tiles.
+  p.pack = a.row_request && a.num_rows > a.num_requests && a.num_rows * (int64_t)c.num_kv_heads >= kPackItems
+               ? max(1, kMaxGroup / p.group) : 1;
+  p.by_group = fast_div(p.group);
   p.scale_log2 = a.scale * 1.44269504088896340736f;
   p.counters = static_cast<int32_t *>(a.workspace);
   p.partials = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kCounterBytes);

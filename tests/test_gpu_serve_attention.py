@@ -266,3 +266,76 @@ def test_cache_in_the_adapters_page_pool(dev):
     c.k, c.v, c.cache, c.layer = k, v, m.make_kv_cache(k, v), 0
     c.run()
     c.check()
+
+
+def with_rows(c, rows, g):
+    """The case's requests with other rows: (request, position) pairs."""
+    dev, hq, d = c.q.device, c.hq, c.q.shape[1] // c.hq
+    c.request = torch.tensor([r for r, _ in rows], dtype=torch.int32, device=dev)
+    c.position = torch.tensor([p for _, p in rows], dtype=torch.int32, device=dev)
+    c.q = torch.empty((len(rows), hq * d), dtype=c.q.dtype, device=dev).normal_(generator=g)
+    c.out_wide = c.out = torch.full((len(rows), hq * d), 77.0, dtype=c.q.dtype, device=dev)
+    c.lse = torch.full((len(rows), hq), 77.0, device=dev)
+    return c
+
+
+@pytest.mark.parametrize("hq, hk, d, pt, dtype", [
+    (1, 1, 64, 16, torch.bfloat16), (8, 8, 128, 16, torch.float16), (15, 5, 80, 24, torch.float16),
+    (32, 8, 128, 32, torch.bfloat16), (8, 1, 128, 16, torch.bfloat16), (12, 1, 64, 8, torch.bfloat16),
+    (10, 2, 256, 16, torch.float16), (40, 2, 64, 16, torch.bfloat16)])
+@pytest.mark.parametrize("window", [0, 1, 30, 400])
+@pytest.mark.parametrize("least", [0, 1100])
+def test_rows_of_one_request_share_its_tiles(dev, hq, hk, d, pt, dtype, window, least):
+    """Prompts, drafted continuations, rows that repeat, go backwards, skip, see nothing or have other requests'
+    rows between them: whatever rows are taken together, each sees its own tokens only."""
+    import random
+    rnd = random.Random(hq * d + window)
+    lens = [1, 5, 40, 300, 1000, 17, 64]
+    c = Case(dev, lens, hq, hk, d, pt, dtype=dtype, window=window, layers=1)
+    rows = [(2, p) for p in range(40)]  # a prompt
+    rows += [(3, p) for p in (295, 296, 297, 298, 299)]  # drafted tokens
+    rows += [(4, 999), (4, 500), (4, 501), (4, 501), (4, 20), (4, 999)]  # gaps, repeats, backwards
+    rows += [(0, 0), (1, 4), (0, 0), (1, 3), (5, 16), (5, -1), (5, 15), (5, 14), (6, 63), (6, 62), (6, 0)]
+    while len(rows) < 150 or len(rows) * hk < least:
+        r = rnd.randrange(7)
+        p = rnd.randrange(lens[r])
+        rows += [(r, min(p + k, lens[r] - 1)) for k in range(rnd.choice((1, 1, 2, 3, 9, 18)))]
+    with_rows(c, rows, torch.Generator(device=dev).manual_seed(5))
+    c.run()
+    assert int(c.status.item()) == 0
+    c.check()
+    first = c.out.clone()
+    c.run()
+    assert torch.equal(c.out, first)
+
+
+@pytest.mark.parametrize("more", [0, 300])
+def test_bad_rows_among_packed_ones(dev, more):
+    c = Case(dev, [100, 200], 4, 4, 64, layers=1)
+    rows = [(0, 97), (0, 98), (0, 99), (0, 10 ** 6), (0, 99), (2, 5), (1, 198), (1, 199), (-1, 3), (1, 199), (1, -2), (1, 7)]
+    rows += [(k % 30 // 15, 40 + k % 15) for k in range(more)]
+    with_rows(c, rows, torch.Generator(device=dev).manual_seed(6))
+    c.run()
+    assert int(c.status.item()) == m.STATUS_BAD_REQUEST | m.STATUS_BAD_LENGTH
+    bad = [3, 5, 8, 10]
+    assert (c.out[bad] == 77).all() and (c.lse[bad] == 77).all()
+    c.check([i for i in range(len(rows)) if i not in bad])
+    # a page that is gone behind every row's window is not looked at
+    c.window = 20
+    rows = [(0, 30), (0, 99), (0, 98), (1, 150), (1, 151)]
+    rows += [(1, 150 + k % 15) for k in range(more)]
+    with_rows(c, rows, torch.Generator(device=dev).manual_seed(7))
+    c.table[0, 3], c.table[1, 0] = -1, -1
+    c.status.zero_()
+    c.run()
+    assert int(c.status.item()) == 0
+    c.check()
+
+
+def test_a_long_prompt_in_pieces_of_many_rows(dev):
+    """2000 rows of one request, more than a launch's, and 3 others."""
+    c = Case(dev, [2100, 50, 3], 8, 2, 128, layers=1)
+    rows = [(0, p) for p in range(100, 2100)] + [(1, 49), (2, 2), (2, 1)]
+    with_rows(c, rows, torch.Generator(device=dev).manual_seed(8))
+    c.run()
+    c.check()

@@ -28,6 +28,8 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "serve.cuh"
 
 namespace mlora {
@@ -59,6 +61,7 @@ struct Vec<MLORA_FP32> {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 4;
 constexpr int kGroup = 4;    // vectors of a thread that are loaded together
 constexpr int kEarlyBias = 2;  // and entries of the list
 constexpr int kEarly = 4;    // tokens of the history that a thread loads ahead
@@ -77,7 +80,7 @@ struct LogitsSmem {
 };
 
 template <int DT, int G>  // G groups of vectors a thread; G = 0: one vector
-__global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_constant__ mlora_logits p, int32_t row0,
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __grid_constant__ mlora_logits p, int32_t row0,
                                                           int32_t *status) {
   using V = Vec<DT>;
   using T = typename V::T;
@@ -322,16 +325,24 @@ cudaError_t launch(const mlora_logits &a, int32_t *status, cudaStream_t stream) 
 template <int DT>
 cudaError_t dispatch(const mlora_logits &a, int32_t *status, cudaStream_t stream) {
   // The longer the slices, the fewer times a row's history is read and counted; the shorter, the more SMs
-  // work. By the CTAs that slices of kGroup vectors a thread would give (fp32: 4096 tokens), an SM's share
-  // of them; measured (us) with slices of 1, 4, 8 and 16 vectors a thread:
-  //   4 x 38319 (40 CTAs): 4.2  5.8  7.5  14.3     24 x 47632 (288): 8.8  6.3  7.5  10.8
-  //   64 x 32000 (512): 14.3  7.5  7.9  10.9       32 x 128001 (1024): 24.6  12.8  11.9  13.8
-  //   64 x 128001 (2048): 48.7  23.5  20.4  18.6   256 x 32000 (2048): 54.3  24.5  20.3  18.3
-  constexpr int kPiece = kThreads * kGroup * Vec<DT>::N;
-  const int64_t ctas = (int64_t)a.num_rows * (((int64_t)a.vocab + kPiece - 1) / kPiece), sms = sm_count();
-  if (ctas < sms) return launch<DT, 0>(a, status, stream);
-  if (ctas < 5 * sms) return launch<DT, 1>(a, status, stream);
-  if (ctas < 10 * sms) return launch<DT, 2>(a, status, stream);
+  // work. All CTAs take about as long, so a last wave of few costs as much as a full one: a call takes
+  // ceil(CTAs / resident) times 4 + vectors a thread. Measured (us) with slices of 1, 4, 8 and 16 vectors
+  // a thread, fp32 unless said; 16-bit slices have twice the tokens:
+  //   4 x 38319: 4.2  5.8  7.5  14.3      24 x 47632: 8.8  6.3  7.5  10.8      64 x 32000: 14.3  7.5  7.9  10.9
+  //   32 x 128001: 24.6  12.8  11.9  13.8    64 x 128001: 48.7  23.5  20.4  18.6   256 x 32000: 54.3  24.5  20.3  18.3
+  //   256 x 128001: -  -  74.8  61.4    256 x 69248: 140  55.4  46.0  47.2
+  //   bf16 8 x 32000: 5.1  6.8  9.7  15.7    fp16 128 x 128001: 56  30  29  27    fp16 213 x 69248: 52  31  36  52
+  const int64_t resident = (int64_t)kCtasPerSm * sm_count();
+  auto cost = [&](int vectors) {
+    const int64_t slice = (int64_t)kThreads * vectors * Vec<DT>::N;
+    const int64_t ctas = (int64_t)a.num_rows * (((int64_t)a.vocab + Vec<DT>::N - 1 + slice - 1) / slice);
+    return (ctas + resident - 1) / resident * (4 + vectors);
+  };
+  const int64_t c0 = cost(1), c1 = cost(kGroup), c2 = cost(2 * kGroup), c4 = cost(4 * kGroup);
+  const int64_t best = std::min(std::min(c0, c1), std::min(c2, c4));
+  if (best == c0) return launch<DT, 0>(a, status, stream);
+  if (best == c1) return launch<DT, 1>(a, status, stream);
+  if (best == c2) return launch<DT, 2>(a, status, stream);
   return launch<DT, 4>(a, status, stream);
 }
 

@@ -14,8 +14,8 @@
 //     list, cut evenly over the SMs and over their warps, so the lengths do not have to match anything and one
 //     long request fills the GPU as well as many short ones. A warp goes from one (row, head) to the
 //     next without draining its ring. Every 32 tiles its lanes work out 32 tiles' places at once.
-//   * Consecutive rows of one request (drafted tokens, a prompt) stand beside each other in a tile's 16 columns, as
-//     many as the group leaves room for, each with a mask of its own (kPackItems has the rule and the figures).
+//   * Consecutive rows of one request (drafted tokens, a prompt) stand beside each other in a tile's columns, as
+//     many as the group leaves room for, each with a mask of its own (kShare8 has the rule and the figures).
 //   * A (row, head) cut between warps is joined in two steps, in a fixed order: the warps of a CTA, in
 //     shared memory, then the CTAs, by the one that finishes last (a counter that it returns to zero).
 // What a warp does between two tiles has to stay below the time its share of the bandwidth gives it
@@ -53,12 +53,14 @@ constexpr int kMaxGroup = 16;        // query heads of a work item
 // and ending one costs, about a tile's products (0.5 us), counts beside the tiles then, not in a call that
 // waits for memory.
 constexpr int kFewTiles = 16;
-// Rows of one request share a tile's columns (a row takes `group` of 16) from this many (row, key-value head)s on, about
-// seven for each SM. It reads a tile once for all of them, at twice the products and longer joins. Measured on 8 heads of
-// 128, group 4, without and with: 32 requests x 4 rows, 500 to 1500 tokens 55.3 and 39.6 us; 64 x 2 69.9 and 52.7;
-// a prompt of 1024 tokens 346 and 179. Below: 8 requests x 4 rows 22.7 and 27.4, 1 x 4 rows of 300 tokens 8.7 and 14.8
-// (but 8 x 4 rows of 2000 to 4000 tokens 45.4 and 35.6: the lengths are not known to the host).
-constexpr int kPackItems = 1024;
+// Rows of one request share a tile's columns, `group` each, where the SMs have at least kShare8 (row, key-value head)s
+// each: up to 8 columns, which costs masks and 1.2 us for the list. From kShare16 on up to 16, twice the products
+// and longer joins, if a request's rows (their average) need them. Measured (us), 8 heads of 128, 500 to 1500 tokens
+// unless said; a row to a tile, 8 columns, 16 columns:
+//   group 4: 4 requests x 4 rows (0.8 an SM) 15.3  18.5  27.2;  8 x 4 (1.7) 22.7  20.0  27.4;  64 x 2 (6.7) 71.6  50.4  54.1;
+//     64 x 5 (17) 142  100  97;  16 x 64 (54) 311  210  171;  a prompt of 256 (13) 23.1  18.4  20.0, of 1024 (54) 346  215  177
+//   group 1: 64 x 8 206  52  56    group 2: 64 x 8 208  76  61    group 8: 32 x 4 (6.7) 56.2  -  58.8
+constexpr int kShare8 = 1, kShare16 = 16;
 constexpr float kSlack = 8.f;        // log2 of how far a weight may pass 1 before m moves
 
 constexpr int attn_warps(int dp) { return dp == 256 ? 4 : 8; }
@@ -905,8 +907,10 @@ cudaError_t launch(const AttnParams &p, int32_t *status, cudaStream_t stream) {
 
 template <int DT, int DP, bool PAGED16>
 cudaError_t dispatch_columns(const AttnParams &p, int32_t *status, cudaStream_t stream) {
-  if (p.pack > 1) return launch<DT, DP, 2, PAGED16, true>(p, status, stream);
-  if (p.group > 8) return launch<DT, DP, 2, PAGED16, false>(p, status, stream);
+  const bool two = p.pack * p.group > 8;
+  if (p.pack > 1)
+    return two ? launch<DT, DP, 2, PAGED16, true>(p, status, stream) : launch<DT, DP, 1, PAGED16, true>(p, status, stream);
+  if (two) return launch<DT, DP, 2, PAGED16, false>(p, status, stream);
   return launch<DT, DP, 1, PAGED16, false>(p, status, stream);
 }
 template <int DT, int DP>
@@ -945,9 +949,9 @@ cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a,
   p.page = fast_div(c.page_tokens);
   p.group = a.num_q_heads / c.num_kv_heads;
   p.chunks = (p.group + kMaxGroup - 1) / kMaxGroup;
-  // A drafted continuation, a prompt: as many of a request's rows as have room beside each other share tiles.
-  p.pack = a.row_request && a.num_rows > a.num_requests && a.num_rows * (int64_t)c.num_kv_heads >= kPackItems
-               ? max(1, kMaxGroup / p.group) : 1;
+  const int64_t per_sm = a.num_rows * (int64_t)c.num_kv_heads / attn_ctas();
+  const int columns = per_sm >= kShare16 && a.num_rows > a.num_requests * (int64_t)(8 / p.group) ? 16 : 8;
+  p.pack = a.row_request && a.num_rows > a.num_requests && per_sm >= kShare8 ? std::max(1, columns / p.group) : 1;
   p.by_group = fast_div(p.group);
   p.scale_log2 = a.scale * 1.44269504088896340736f;
   p.counters = static_cast<int32_t *>(a.workspace);

@@ -284,7 +284,7 @@ def with_rows(c, rows, g):
     (32, 8, 128, 32, torch.bfloat16), (8, 1, 128, 16, torch.bfloat16), (12, 1, 64, 8, torch.bfloat16),
     (10, 2, 256, 16, torch.float16), (40, 2, 64, 16, torch.bfloat16)])
 @pytest.mark.parametrize("window", [0, 1, 30, 400])
-@pytest.mark.parametrize("least", [0, 1100])
+@pytest.mark.parametrize("least", [0, 1100, 2600])
 def test_rows_of_one_request_share_its_tiles(dev, hq, hk, d, pt, dtype, window, least):
     """Prompts, drafted continuations, rows that repeat, go backwards, skip, see nothing or have other requests'
     rows between them: whatever rows are taken together, each sees its own tokens only."""

@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
           for (int nb = 0; nb < NB; ++nb) mma<DT>(kk & 1 ? s2[h][nb] : s[h][nb], x, q[kk][nb][0], q[kk][nb][1]);
         }
       // s[h][nb][2 i + j]: token 16 h + g + 8 i, head quad * 2 + j
-      bool past = false;
+      bool past = false, part = false;  // part: a token that only some columns see
 #pragma unroll
       for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -592,11 +592,46 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
             bool on = ((seen >> (16 * h + g + 8 * (j >> 1))) & 1u) != 0;
             if (PACK) {
               const int t = token + 16 * h + 8 * (j >> 1), last = sees[nb][j & 1];
-              on = on && t <= last && t >= low_of(last);
+              const bool sees_it = t <= last && t >= low_of(last);
+              part |= on && !sees_it;
+              on = on && sees_it;
             }
             s[h][nb][j] = on ? (s[h][nb][j] + s2[h][nb][j]) * p.scale_log2 : -CUDART_INF_F;
             past |= s[h][nb][j] > m[nb][j & 1] + kSlack;
           }
+      if (PACK && __any_sync(~0u, part)) {
+        // A column that does not see a token has its weight 0, and 0 times an infinity or NaN of its V is NaN. Those
+        // elements go to the columns that do see them by themselves (whatever the weight) and leave the tile.
+        uint16_t *const v = sh.ring[warp][slot] + kTile * DP;
+        constexpr uint32_t kExp = DT == MLORA_FP16 ? 0x7C00u : 0x7F80u;  // all ones: an infinity or NaN
+        auto wild = [&](uint32_t x) { return (x & kExp) == kExp; };
+        bool some = false;
+        for (int i = lane; i < kTile * DP / 2; i += 32) {
+          const uint32_t x = reinterpret_cast<const uint32_t *>(v)[i];
+          some |= wild(x) || wild(x >> 16);
+        }
+        if (__any_sync(~0u, some)) {
+#pragma unroll 1
+          for (int t = 0; t < kTile; ++t) {
+            const int at = token - g + t;
+#pragma unroll
+            for (int j = 0; j < DP / 8; ++j) {
+              const uint32_t x = v[t * DP + ((j ^ (t & 7)) << 3) + g];  // element 8 j + g
+              if (!wild(x)) continue;
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (((seen >> t) & 1u) && at <= sees[nb][i] && at >= low_of(sees[nb][i]))
+                    o[j / 2][nb][(j & 1) * 2 + i] += Elem<DT>::lo(x);
+            }
+          }
+          __syncwarp();
+          for (int i = lane; i < kTile * DP; i += 32)
+            if (wild(v[i])) v[i] = 0;
+          __syncwarp();
+        }
+      }
       token += kTile;
       if (__any_sync(~0u, past)) {  // m moves to the maximum
 #pragma unroll

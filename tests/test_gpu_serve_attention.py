@@ -339,3 +339,34 @@ def test_a_long_prompt_in_pieces_of_many_rows(dev):
     with_rows(c, rows, torch.Generator(device=dev).manual_seed(8))
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("hq, hk, d, pt, dtype", [
+    (4, 2, 128, 16, torch.bfloat16), (15, 5, 80, 24, torch.float16), (32, 16, 64, 16, torch.float16),
+    (32, 16, 128, 8, torch.bfloat16), (16, 16, 256, 16, torch.bfloat16), (128, 16, 128, 16, torch.float16)])
+@pytest.mark.parametrize("window", [0, 37])
+def test_a_value_that_only_later_rows_see(dev, hq, hk, d, pt, dtype, window):
+    """Infinities and NaN in a token's V reach the rows that see it, at those elements, and no other."""
+    c = Case(dev, [260, 90], hq, hk, d, pt, dtype=dtype, window=window, layers=1)
+    rows = [(0, p) for p in range(60, 260)] + [(1, p) for p in range(70, 90)]
+    with_rows(c, rows, torch.Generator(device=dev).manual_seed(9))
+    wild = {(0, 100): (float("inf"), [0, d - 1]), (0, 163): (float("nan"), [5]), (0, 164): (float("-inf"), [d // 2]),
+            (0, 259): (float("nan"), list(range(d))), (1, 80): (float("inf"), [1])}
+    for (r, t), (x, els) in wild.items():
+        c.v[c.layer, int(c.table[r, t // pt]), t % pt, :, els] = x
+    c.run()
+    assert int(c.status.item()) == 0
+    out = c.out.reshape(-1, hq, d)
+    for (r, t), (x, els) in wild.items():
+        c.v[c.layer, int(c.table[r, t // pt]), t % pt, :, els] = 0
+    want, lse, tol, ltol = ref.attention(c.q.reshape(-1, hq, d), c.k, c.v, c.layer, c.table, c.request, c.position, c.scale,
+                                         window)
+    ref.assert_within(c.lse, lse, ltol, "lse")
+    hit = torch.zeros((len(rows), d), dtype=torch.bool, device=dev)
+    for i, (r, p) in enumerate(rows):
+        for (wr, t), (_, els) in wild.items():
+            if wr == r and (max(0, p + 1 - window) if window else 0) <= t <= p:
+                hit[i, els] = True
+    hit = hit[:, None, :].expand(-1, hq, -1)
+    assert not torch.isfinite(out[hit]).any()
+    ref.assert_within(out[~hit], want[~hit], tol[~hit], "out")

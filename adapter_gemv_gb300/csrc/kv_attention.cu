@@ -57,10 +57,12 @@ constexpr int kFewTiles = 16;
 // each: up to 8 columns, which costs masks and 1.2 us for the list. From kShare16 on up to 16, twice the products
 // and longer joins, if a request's rows (their average) need them. Measured (us), 8 heads of 128, 500 to 1500 tokens
 // unless said; a row to a tile, 8 columns, 16 columns:
-//   group 4: 4 requests x 4 rows (0.8 an SM) 15.3  18.5  27.2;  8 x 4 (1.7) 22.7  20.0  27.4;  64 x 2 (6.7) 71.6  50.4  54.1;
-//     64 x 5 (17) 142  100  97;  16 x 64 (54) 311  210  171;  a prompt of 256 (13) 23.1  18.4  20.0, of 1024 (54) 346  215  177
-//   group 1: 64 x 8 206  52  56    group 2: 64 x 8 208  76  61    group 8: 32 x 4 (6.7) 56.2  -  58.8
-constexpr int kShare8 = 1, kShare16 = 16;
+//   group 4: 4 requests x 4 rows (0.8 an SM) 15.3  17.6  22.9;  8 x 4 (1.7) 22.6  18.8  24.2;  64 x 2 (6.7) 71.7  49.9  52.2;
+//     32 x 4 (6.7) 55.1  39.7  38.9;  64 x 5 (17) 142  98  83;  16 x 64 (54) 305  189  137;
+//     a prompt of 256 (13) 23.1  18.6  19.0, of 1024 (54) 347  232  182
+//   group 1: 64 x 8 205  52  54    group 2: 64 x 8 207  75  59    group 8: 32 x 4 (6.7) 55.9  -  50.6
+//   group 3, 37 x 3 short ones (3.6) 25.0  23.0  25.6
+constexpr int kShare8 = 1, kShare16 = 6;
 constexpr float kSlack = 8.f;        // log2 of how far a weight may pass 1 before m moves
 
 constexpr int attn_warps(int dp) { return dp == 256 ? 4 : 8; }

@@ -126,6 +126,18 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 0, or NaN where one of the four is an infinity or NaN
+__device__ __forceinline__ float odd(const float4 &f) { return (f.x * 0.f + f.y * 0.f) + (f.z * 0.f + f.w * 0.f); }
+
+// acc += x f for a piece's elements f. An infinity or NaN among them, which has come from V, stays what it is when
+// the piece's weight x is below the smallest number (where x f is NaN).
+__device__ __forceinline__ void add_weighed(float4 &acc, float x, const float4 &f) {
+  acc.x += x == 0.f && f.x * 0.f != 0.f ? f.x : x * f.x;
+  acc.y += x == 0.f && f.y * 0.f != 0.f ? f.y : x * f.y;
+  acc.z += x == 0.f && f.z * 0.f != 0.f ? f.z : x * f.z;
+  acc.w += x == 0.f && f.w * 0.f != 0.f ? f.w : x * f.w;
+}
+
 // (x, y) rounded to a pair, and the pair of what the rounding left.
 template <int DT>
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint32_t &lo) {
@@ -176,6 +188,109 @@ struct AttnSmem {
   int32_t piece_row[2 * NW], piece_hc[2 * NW];
   int32_t last[2];
 };
+
+// The last row with first[row] HC <= x, for x below the list's length.
+__device__ __forceinline__ int row_of(const int32_t *first, int rows, int HC, int x) {
+  int r = 0;
+  for (int hi = rows; hi - r > 1;) {
+    const int mid = (r + hi) >> 1;
+    if (first[mid] * HC <= x) r = mid;
+    else hi = mid;
+  }
+  return r;
+}
+
+// Columns of the item (row r, head and chunk hc), and the first's query head. rows: a pack's, by its first row.
+template <bool PACK>
+__device__ __forceinline__ int columns(const AttnParams &p, const uint8_t *rows, int r, int hc, int64_t &head0) {
+  const int hk = p.chunks == 1 ? hc : hc / p.chunks, g0 = p.chunks == 1 ? 0 : (hc - hk * p.chunks) * kMaxGroup;
+  head0 = (int64_t)hk * p.group + g0;
+  if (PACK) return rows[r] * p.group;  // (one chunk)
+  return min(p.group - g0, kMaxGroup);
+}
+
+template <int DT>
+__device__ __forceinline__ bool is_wild(uint32_t x) {  // the 16-bit number in its low half is an infinity or NaN
+  constexpr uint32_t kExp = DT == MLORA_FP16 ? 0x7C00u : 0x7F80u;
+  return (x & kExp) == kExp;
+}
+
+// An infinity or NaN in a token's V. The products leave NaN for an infinity as soon as a part of its weight is 0 (what
+// remains of an exact weight) or negative (a remainder), or o is rescaled by 0. So where a piece's o is not finite, the V
+// of the warp's pieces are read again, and an element that holds infinities or NaN becomes their sum over the tokens that
+// the column sees: whatever a weight above 0 is, an infinity with it is that infinity. The others stay as they are. Twice
+// over the tokens, to clear such elements where they have been left and to sum them there. Tiles w0 .. w0 + n - 1 of the
+// list are the warp's. (A function of its own: inside the kernel its registers were the loop's, and 4 requests of 512
+// rows took 457 us instead of 434.)
+template <int DT, int DP, int NB, bool PACK>
+__device__ __noinline__ void mend_values(const AttnParams &p, AttnSmem<DP, attn_warps(DP), NB, PACK> &sh, int w0, int n,
+                                         int empty) {
+  constexpr int kTile = AttnSmem<DP, attn_warps(DP), NB, PACK>::kTile;
+  const mlora_kv_attn &a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.c.head_dim, HC = p.c.num_kv_heads * p.chunks;
+  auto low_of = [&](int pos) { return a.window ? max(0, pos + 1 - a.window) : 0; };
+  auto wild2 = [&](uint32_t x) { return is_wild<DT>(x) || is_wild<DT>(x >> 16); };
+  __syncwarp();
+#pragma unroll 1
+  for (int x = w0; x < w0 + n;) {
+    const int r = row_of(sh.first, p.rows, HC, x), nt = sh.first[r + 1] - sh.first[r], rem = x - sh.first[r] * HC;
+    const int item = quick_div(rem, nt), tile0 = rem - item * nt, tiles = min(nt - empty - tile0, w0 + n - x);
+    x += nt - tile0;
+    if (tiles <= 0) continue;
+    const bool whole = tile0 == 0 && tiles == nt - empty;
+    float *const part = tile0 == 0 ? reinterpret_cast<float *>(sh.ring[warp]) : sh.head[warp][0];
+    const int high = PACK ? sh.high[r] : sh.pos[r], low = PACK ? sh.low[r] : low_of(high);
+    const int from = max(low, (low / kTile + tile0) * kTile), last = (low / kTile + tile0 + tiles - 1) * kTile;
+    const int tokens = last - from + min(high - last, kTile - 1) + 1;
+    int64_t head0;
+    const int cols = columns<PACK>(p, sh.rows, r, item, head0);
+    const int32_t *const pages = a.page_table + (int64_t)sh.req[r] * a.table_stride;
+    const uint16_t *const v = p.v + (int64_t)(p.chunks == 1 ? item : item / p.chunks) * p.c.head_stride;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass)
+#pragma unroll 1
+      for (int i0 = 0; i0 < tokens; i0 += 32) {
+        // a lane's token: whether its V holds any
+        const uint16_t *mine = v;
+        bool some = false;
+        if (i0 + lane < tokens) {
+          const int t = from + i0 + lane, pg = div_by(p.page, t), id = pages[pg];
+          if (id >= 0 && id < p.c.num_pages) {
+            mine += (int64_t)id * p.c.page_stride + (int64_t)(t - pg * p.page.d) * p.c.token_stride;
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+              const uint4 y = ldg_u4(mine + i * 8);
+              some |= wild2(y.x) || wild2(y.y) || wild2(y.z) || wild2(y.w);
+            }
+          }
+        }
+#pragma unroll 1
+        for (uint32_t left = __ballot_sync(~0u, some); left; left &= left - 1) {
+          const int k = __ffs(left) - 1, t = from + i0 + k;
+          const uint16_t *const of =
+              reinterpret_cast<const uint16_t *>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(mine), k));
+#pragma unroll 1
+          for (int d = lane; d < D; d += 32) {  // (a lane comes back to the elements that it has cleared)
+            const uint32_t y = of[d];
+            if (!is_wild<DT>(y)) continue;
+#pragma unroll 1
+            for (int c = 0; c < cols; ++c) {
+              const int row = r + (PACK ? div_by(p.by_group, c) : 0);
+              if (PACK && (t > sh.pos[row] || t < low_of(sh.pos[row]))) continue;
+              if (whole) {
+                uint16_t *const to = static_cast<uint16_t *>(a.out) + ((int64_t)p.row0 + row) * a.ldo +
+                                     (head0 + c - (row - r) * p.group) * D + d;
+                *to = pass ? Elem<DT>::from_float(Elem<DT>::lo(*to) + Elem<DT>::lo(y)) : (uint16_t)0;
+              } else {
+                float &to = part[c * DP + d];
+                to = pass ? to + Elem<DT>::lo(y) : 0.f;
+              }
+            }
+          }
+        }
+      }
+  }
+}
 
 // PAGED16: a page holds whole tiles. NB: blocks of 8 columns (heads of a group's chunk). PACK: rows of one request share
 // them.
@@ -303,16 +418,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
     const int longer = rest * (share + 1);
     return tile < longer ? quick_div(tile, share + 1) : rest + quick_div(tile - longer, share);
   };
-  // the last row with first[row] HC <= x, for x < T
-  auto row_of = [&](int x) {
-    int r = 0;
-    for (int hi = R; hi - r > 1;) {
-      const int mid = (r + hi) >> 1;
-      if (sh.first[mid] * HC <= x) r = mid;
-      else hi = mid;
-    }
-    return r;
-  };
+  auto row_of = [&](int x) { return mlora::row_of(sh.first, R, HC, x); };
   int t0, t1;
   {
     int x = first_of(blockIdx.x + (lane & 1));  // lanes 0 and 1: the CTA's two boundaries
@@ -333,12 +439,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
 
   // The columns of an item (row r, head and chunk hc): the query heads of its chunk, or those of its pack's rows. Head
   // head0 of row r is the first; column c is head in(c) behind it, of row below(c) behind r.
-  auto columns = [&](int r, int hc, int64_t &head0) {
-    const int hk = p.chunks == 1 ? hc : hc / p.chunks, g0 = p.chunks == 1 ? 0 : (hc - hk * p.chunks) * kMaxGroup;
-    head0 = (int64_t)hk * p.group + g0;
-    if (PACK) return sh.rows[r] * p.group;  // (one chunk)
-    return min(p.group - g0, kMaxGroup);
-  };
+  auto columns = [&](int r, int hc, int64_t &head0) { return mlora::columns<PACK>(p, sh.rows, r, hc, head0); };
   auto below = [&](int c) { return PACK ? div_by(p.by_group, c) : 0; };
   auto in = [&](int c) { return c - below(c) * p.group; };
   auto lse_of = [&](float m, float l) { return l == 0.f ? -CUDART_INF_F : (m - kShift) * CUDART_LN2_F + logf(l); };
@@ -510,6 +611,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
             ahead[kk][nb][j] = nb * 8 + g < cols && d < D ? *reinterpret_cast<const uint32_t *>(qr[nb] + d) : 0u;
           }
     };
+    bool mend = false;  // a piece's o holds an infinity or NaN
     constexpr bool kAhead = DP * NB < 512;  // (no registers left for it at 16 heads of 256)
     float o[DP / 16][NB][4];     // O^T: elements j * 16 + g (0, 1) and + 8 (2, 3), heads quad * 2 + {0, 1}
     float m[NB][2], l[NB][2];    // of heads quad * 2 + {0, 1}; l: of this lane's tokens
@@ -603,14 +705,12 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
           }
       if (PACK && __any_sync(~0u, part)) {
         // A column that does not see a token has its weight 0, and 0 times an infinity or NaN of its V is NaN. Those
-        // elements go to the columns that do see them by themselves (whatever the weight) and leave the tile.
+        // elements leave the tile and mark the columns that do see them (mend_values goes by that).
         uint16_t *const v = sh.ring[warp][slot] + kTile * DP;
-        constexpr uint32_t kExp = DT == MLORA_FP16 ? 0x7C00u : 0x7F80u;  // all ones: an infinity or NaN
-        auto wild = [&](uint32_t x) { return (x & kExp) == kExp; };
         bool some = false;
         for (int i = lane; i < kTile * DP / 2; i += 32) {
           const uint32_t x = reinterpret_cast<const uint32_t *>(v)[i];
-          some |= wild(x) || wild(x >> 16);
+          some |= is_wild<DT>(x) || is_wild<DT>(x >> 16);
         }
         if (__any_sync(~0u, some)) {
 #pragma unroll 1
@@ -619,7 +719,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
 #pragma unroll
             for (int j = 0; j < DP / 8; ++j) {
               const uint32_t x = v[t * DP + ((j ^ (t & 7)) << 3) + g];  // element 8 j + g
-              if (!wild(x)) continue;
+              if (!is_wild<DT>(x)) continue;
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -630,7 +730,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
           }
           __syncwarp();
           for (int i = lane; i < kTile * DP; i += 32)
-            if (wild(v[i])) v[i] = 0;
+            if (is_wild<DT>(v[i])) v[i] = 0;
           __syncwarp();
         }
       }
@@ -699,6 +799,16 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
             l[nb][j] += __shfl_xor_sync(~0u, l[nb][j], 8);
             l[nb][j] += __shfl_xor_sync(~0u, l[nb][j], 16);
           }
+        {
+          float not_finite[4] = {};  // 0, or NaN where o holds an infinity or NaN
+#pragma unroll
+          for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) not_finite[j] = fmaf(o[i][nb][j], 0.f, not_finite[j]);
+          mend |= __any_sync(~0u, (not_finite[0] + not_finite[1]) + (not_finite[2] + not_finite[3]) != 0.f) != 0;
+        }
         if ((meta & kLast) && with_first) {  // and whole
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
@@ -748,6 +858,7 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       }
     }
     cp_async_wait<0>();
+    if (mend) mend_values<DT, DP, NB, PACK>(p, sh, w0, n, empty);
   }
   if (!__syncthreads_or(pieces)) return;
 
@@ -824,13 +935,25 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
       for (int i0 = 0; i0 < DP / 4; i0 += 32) {
         const int i = i0 + lane;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto piece = [&](int e) {
+          return reinterpret_cast<const float4 *>(e & 1 ? reinterpret_cast<const float *>(sh.ring[e >> 1])
+                                                        : sh.head[e >> 1][0])[head * (DP / 4) + i];
+        };
         for (uint32_t left = pieces_of; left; left &= left - 1) {
           const int e = __ffs(left) - 1;
           const float x = __shfl_sync(~0u, w, e);
           if (i < DP / 4) {
-            const float4 f = reinterpret_cast<const float4 *>(e & 1 ? reinterpret_cast<const float *>(sh.ring[e >> 1])
-                                                                    : sh.head[e >> 1][0])[head * (DP / 4) + i];
+            const float4 f = piece(e);
             acc.x += x * f.x, acc.y += x * f.y, acc.z += x * f.z, acc.w += x * f.w;
+          }
+        }
+        if (__any_sync(~0u, odd(acc) != 0.f)) {
+          acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (uint32_t left = pieces_of; left; left &= left - 1) {
+            const int e = __ffs(left) - 1;
+            const float x = __shfl_sync(~0u, w, e);
+            if (i < DP / 4) add_weighed(acc, x, piece(e));
           }
         }
         if (i >= DP / 4) continue;
@@ -911,6 +1034,18 @@ __global__ void __launch_bounds__(attn_warps(DP) * 32, 1)
             const float x = __shfl_sync(~0u, w, k);
             acc[i].x += x * f.x, acc[i].y += x * f.y, acc[i].z += x * f.z, acc[i].w += x * f.w;
           }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < (DP + 127) / 128; ++i) {
+        if (!__any_sync(~0u, odd(acc[i]) != 0.f)) continue;
+        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i * 32 + lane >= DP / 4) continue;
+#pragma unroll 1
+        for (int k = 0; k < count; ++k) {
+          const float m = __ldcg(at(k) + kMaxGroup * DP + head), base = top == -CUDART_INF_F ? 0.f : top;
+          add_weighed(acc[i], exp2_fast(m - base),
+                      __ldcg(reinterpret_cast<const float4 *>(at(k)) + head * (DP / 4) + i * 32 + lane));
         }
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;

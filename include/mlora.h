@@ -392,7 +392,9 @@ MLORA_API int lora_kv_append(const mlora_kv_cache *cache, const mlora_kv_rows *r
  * the scores, the sums and the softmax's statistics in fp32, the output rounded once. A row with
  * position -1 sees nothing: its output is 0 and its lse -inf. Several rows of one request (a drafted
  * continuation, the rows of a prompt) are rows of their own. Cache contents outside the tokens that a
- * row sees, NaN included, do not reach its output. The long rows' tokens are split over the whole GPU
+ * row sees, NaN included, do not reach its output. An element of V that is an infinity makes the output's that infinity,
+ * however small the token's weight; a NaN, or infinities of both signs, make it NaN. A row whose every score is -inf has
+ * no weights: its output is 0 and its lse -inf. The long rows' tokens are split over the whole GPU
  * and joined in a fixed order: the same call gives the same bits.
  * workspace: lora_kv_attention_workspace bytes of device memory, 16-byte aligned, zeroed by the
  * caller before its first use; every call leaves the part that has to be zero at zero. Calls that may

@@ -125,11 +125,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
   if (!bad) {
     if (p.total_len) {
       total = p.total_len[r], prompt = p.prompt_len[r];
-      text = p.tokens + (int64_t)r * p.tokens_stride;  // (the array's rows are tokens_stride long)
+      text = p.tokens + (int64_t)r * p.tokens_stride;
 #pragma unroll
       for (int k = 0; k < kEarly; ++k)
-        if (k * kThreads + tid < p.tokens_stride) early[k] = text[k * kThreads + tid];
-      if (total < 0 || total > p.tokens_stride || prompt < 0 || prompt > total) bad |= MLORA_STATUS_BAD_LENGTH;
+        if (k * kThreads + tid < p.tokens_len) early[k] = text[k * kThreads + tid];
+      if (total < 0 || total > p.tokens_len || prompt < 0 || prompt > total) bad |= MLORA_STATUS_BAD_LENGTH;
     }
     if (p.bias_offsets) {
       bias0 = p.bias_offsets[r], bias1 = p.bias_offsets[r + 1];

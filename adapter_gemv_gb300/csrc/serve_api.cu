@@ -146,7 +146,8 @@ int lora_logits_adjust(const mlora_logits *a, int32_t *dev_status, void *stream)
   if (!a->bias_offsets && (a->bias_token || a->bias_value)) return MLORA_ERR_NULL;
   if (a->bias_offsets && a->num_bias > 0 && (!a->bias_token || !a->bias_value)) return MLORA_ERR_NULL;
   if (!a->mask != !a->mask_index) return MLORA_ERR_NULL;
-  if (a->total_len && (a->tokens_stride < 0 || a->tokens_stride > INT32_MAX)) return MLORA_ERR_SHAPE;
+  if (a->total_len && (a->tokens_stride < 0 || a->tokens_len < 0 || a->tokens_len > a->tokens_stride)) return MLORA_ERR_SHAPE;
+  if (a->total_len && !a->tokens_len && a->tokens_stride > INT32_MAX) return MLORA_ERR_SHAPE;
   if (a->bias_offsets && a->num_bias < 0) return MLORA_ERR_SHAPE;
   if (a->mask && (a->num_masks < 1 || a->mask_stride < ((int64_t)a->vocab + 31) / 32)) return MLORA_ERR_SHAPE;
   const uintptr_t elem = a->dtype == MLORA_FP32 ? 4 : 2;
@@ -154,7 +155,9 @@ int lora_logits_adjust(const mlora_logits *a, int32_t *dev_status, void *stream)
       !all_aligned(4, a->row_request, a->tokens, a->prompt_len, a->total_len, a->repetition, a->presence, a->frequency,
                    a->temperature, a->bias_offsets, a->bias_token, a->bias_value, a->mask, a->mask_index, dev_status))
     return MLORA_ERR_ALIGN;
-  return done(mlora::launch_logits_adjust(*a, dev_status, static_cast<cudaStream_t>(stream)), "logits launch");
+  mlora_logits b = *a;
+  if (b.total_len && !b.tokens_len) b.tokens_len = (int32_t)b.tokens_stride;
+  return done(mlora::launch_logits_adjust(b, dev_status, static_cast<cudaStream_t>(stream)), "logits launch");
 }
 
 }  // extern "C"

@@ -60,7 +60,7 @@ class mlora_logits(ctypes.Structure):
                 ("ld", _L), ("ldo", _L), ("row_request", _V), ("tokens", _V), ("tokens_stride", _L), ("prompt_len", _V),
                 ("total_len", _V), ("repetition", _V), ("presence", _V), ("frequency", _V), ("temperature", _V),
                 ("bias_offsets", _V), ("bias_token", _V), ("bias_value", _V), ("num_bias", _I), ("mask", _V),
-                ("mask_stride", _L), ("mask_index", _V), ("num_masks", _I)]
+                ("mask_stride", _L), ("mask_index", _V), ("num_masks", _I), ("tokens_len", _I)]
 
 
 _PC = ctypes.POINTER(mlora_kv_cache)
@@ -282,7 +282,9 @@ class LogitsAdjust:
         s.row_request = _vec(row_request, "row_request", rows)
         if tokens is not None:
             s.tokens = tokens.data_ptr()
-            s.tokens_stride = _matrix(tokens, "tokens", torch.int32, n, 0)
+            s.tokens_stride, s.tokens_len = _matrix(tokens, "tokens", torch.int32, n, 0), int(tokens.shape[1])
+            if not s.tokens_len:
+                s.tokens_stride = 0  # (a length of 0 alone would mean the stride)
         s.prompt_len, s.total_len = _vec(prompt_len, "prompt_len", n), _vec(total_len, "total_len", n)
         for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency),
                         ("temperature", temperature)):

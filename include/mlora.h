@@ -436,9 +436,10 @@ MLORA_API int lora_kv_attention(const mlora_kv_cache *cache, const mlora_kv_attn
  *   mask_index[r] >= 0 and bit t % 32 of mask[mask_index[r]][t / 32] is 0: x = -inf
  * Every array may be NULL and then has no part (tokens, prompt_len and total_len together; bias_offsets,
  * bias_token and bias_value; mask and mask_index). logits and out are rows ld, ldo elements apart, aligned
- * to their element; out may be logits.
+ * to their element; out may be logits. Every id of a row of tokens may be read, those behind its total_len included (a
+ * matrix that is part of a wider one has its own width as tokens_len).
  * Status: a token id outside [0, vocab) in a history or a bias list (BAD_TOKEN): that entry has no
- * part. total_len[r] outside [0, tokens_stride] or prompt_len[r] outside [0, total_len[r]] or bias offsets
+ * part. total_len[r] outside [0, tokens_len] or prompt_len[r] outside [0, total_len[r]] or bias offsets
  * that decrease or leave [0, num_bias] (BAD_LENGTH), mask_index[r] outside [-1, num_masks) (BAD_SLOT), row_request[i]
  * outside [-1, num_requests) (BAD_REQUEST): the row is skipped. */
 typedef struct {
@@ -448,7 +449,7 @@ typedef struct {
   void *out;
   int64_t ld, ldo;
   const int32_t *row_request;     /* [num_rows], or NULL: row i is request i */
-  const int32_t *tokens;          /* [num_requests][tokens_stride] */
+  const int32_t *tokens;          /* [num_requests] rows of tokens_len ids, tokens_stride apart */
   int64_t tokens_stride;
   const int32_t *prompt_len, *total_len;                        /* [num_requests] */
   const float *repetition, *presence, *frequency, *temperature; /* [num_requests] each */
@@ -460,6 +461,7 @@ typedef struct {
   int64_t mask_stride;
   const int32_t *mask_index;      /* [num_requests] */
   int32_t num_masks;
+  int32_t tokens_len;             /* ids in a row of tokens, at most tokens_stride; 0: tokens_stride of them */
 } mlora_logits;
 
 MLORA_API int lora_logits_adjust(const mlora_logits *args, int32_t *dev_status, void *stream);

@@ -214,3 +214,34 @@ def test_temperatures_of_all_sizes(dev, dtype):
     tiny = want.float().abs() < 1e-37  # (rounded again below the normal numbers)
     assert torch.equal(out[~tiny], want[~tiny])
     assert ((out.double() - want.double()).abs()[tiny] <= 2e-45).all() or dtype != torch.float32
+
+
+@pytest.mark.parametrize("first", [0, 3, 400, 511])
+@pytest.mark.parametrize("alone", [False, True])
+def test_history_in_a_column_view(dev, first, alone):
+    """tokens as columns of a wider matrix, up to its very end: a row's ids are the view's, and a total_len beyond them is
+    an error although the matrix's rows go on."""
+    history = 512 - first
+    a = make(1 if alone else 5, 3001, torch.float32, history, 4)
+    a["total_len"][:] = history
+    a["prompt_len"][:] = history // 2
+    n = a["x"].shape[0]
+    wide = torch.full((7, 512), 17, dtype=torch.int32, device=dev)
+    view = wide[7 - n:, first:]
+    view.copy_(a["tokens"])
+    kw = {k: a[k].to(dev) for k in NAMES if k != "tokens"}
+    kw["bias"] = tuple(t.to(dev) for t in a["bias"])
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    x = a["x"].to(dev)
+    out = torch.full_like(x, 55.0)
+    m.lora_logits_adjust(out, x, tokens=view, status=st, **kw)
+    assert int(st.item()) == 0
+    check(a, out.cpu())
+    if n > 1:  # one id more than row 1 has: the first of the next row, if the matrix's rows were taken for the view's
+        kw["total_len"][1] = history + 1
+        out.fill_(55.0)
+        m.lora_logits_adjust(out, x, tokens=view, status=st, **kw)
+        want, tol = ref.logits(**a)
+        keep = [0, 2, 3, 4]
+        ref.assert_within(out.cpu()[keep], want[keep], tol[keep], "logits")
+        assert int(st.item()) == m.STATUS_BAD_LENGTH and (out[1] == 55).all()

@@ -1,0 +1,45 @@
+"""What the serving operators may read and write, as far as the host decides it: the sizes that the binding passes on,
+and arguments that would leave the arrays or let rows overwrite each other (CPU only)."""
+import ctypes
+
+import pytest
+import torch
+
+import adapter_gemv_gb300 as m
+from adapter_gemv_gb300 import serve
+from test_serve_abi import LOGITS, L, made  # noqa: F401
+
+
+@pytest.fixture
+def host_tensors(monkeypatch):
+    """The binding takes host tensors for device ones; nothing is called with them."""
+    at = lambda t, what, dtype=None: 0 if t is None else t.data_ptr()  # noqa: E731
+    monkeypatch.setattr(m, "_dev", at)
+    monkeypatch.setattr(serve, "_dev", at)
+
+
+def logits_call(tokens, n):
+    x, i = torch.zeros(n, 40), torch.zeros(n, dtype=torch.int32)
+    return m.LogitsAdjust(x, x, tokens=tokens, prompt_len=i, total_len=i).struct
+
+
+@pytest.mark.parametrize("first", [0, 1, 100, 199, 200])
+@pytest.mark.parametrize("rows", [1, 3])
+def test_a_history_that_is_part_of_a_wider_matrix(L, host_tensors, rows, first):  # noqa: F811
+    """Rows are as long as the view is wide, not as far apart as the matrix's."""
+    wide = torch.zeros((rows, 200), dtype=torch.int32)
+    s = logits_call(wide[:, first:], rows)
+    assert s.tokens_len == 200 - first
+    assert s.tokens_stride >= s.tokens_len
+    if first < 200:
+        end = (rows - 1) * s.tokens_stride + s.tokens_len  # behind the last id that may be read
+        assert s.tokens + 4 * end == wide.data_ptr() + 4 * wide.numel()
+    else:
+        assert s.tokens_stride == 0
+
+
+@pytest.mark.parametrize("kw", [dict(tokens_len=-1), dict(tokens_len=8), dict(tokens_stride=1 << 31),
+                                dict(tokens_stride=0, tokens_len=1)])
+def test_history_lengths_are_refused(L, kw):  # noqa: F811
+    s = made(m.mlora_logits, LOGITS, kw)
+    assert L.lora_logits_adjust(ctypes.byref(s), None, None) == m.ERR_SHAPE

@@ -70,6 +70,7 @@ constexpr uint32_t kInPrompt = 0x80000000u;
 
 template <int SLICE>
 struct LogitsSmem {
+  static_assert(SLICE + 8 <= INT32_MAX - MLORA_LOGITS_MAX_VOCAB, "tokens up to a slice's end are counted in 31 bits");
   static constexpr int kWords = SLICE / 32;
   uint32_t grammar[kWords + 1];  // the mask's bits of the slice, from the word of its first token
   uint32_t hit[kWords];          // tokens of the history or the list

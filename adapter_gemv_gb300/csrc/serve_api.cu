@@ -136,7 +136,7 @@ int lora_kv_attention(const mlora_kv_cache *cache, const mlora_kv_attn *a, int32
 int lora_logits_adjust(const mlora_logits *a, int32_t *dev_status, void *stream) {
   if (!a) return MLORA_ERR_NULL;
   if (a->dtype != MLORA_BF16 && a->dtype != MLORA_FP16 && a->dtype != MLORA_FP32) return MLORA_ERR_DTYPE;
-  if (a->num_rows < 0 || a->vocab < 1 || a->num_requests < 0) return MLORA_ERR_SHAPE;
+  if (a->num_rows < 0 || a->vocab < 1 || a->vocab > MLORA_LOGITS_MAX_VOCAB || a->num_requests < 0) return MLORA_ERR_SHAPE;
   if (a->num_rows == 0) return MLORA_OK;
   if (!a->logits || !a->out) return MLORA_ERR_NULL;
   if (a->ld < a->vocab || a->ldo < a->vocab) return MLORA_ERR_SHAPE;

@@ -295,6 +295,7 @@ MLORA_API int lora_sgmv_sequence(const mlora_group *groups, int32_t num_groups, 
 
 #define MLORA_KV_MAX_REQUESTS 8192
 #define MLORA_KV_MAX_HEAD_DIM 256
+#define MLORA_LOGITS_MAX_VOCAB (INT32_MAX - 65536) /* a slice of a row ends at most 32768 + 8 tokens behind it */
 
 /* lora_kv_layout: from the requests' lengths, on the GPU, the pages they take or give back, and the
  * places of the step's rows. With n = new_tokens[r] and len = kv_len[r] of request r:
@@ -443,7 +444,7 @@ MLORA_API int lora_kv_attention(const mlora_kv_cache *cache, const mlora_kv_attn
  * that decrease or leave [0, num_bias] (BAD_LENGTH), mask_index[r] outside [-1, num_masks) (BAD_SLOT), row_request[i]
  * outside [-1, num_requests) (BAD_REQUEST): the row is skipped. */
 typedef struct {
-  int32_t num_rows, vocab, dtype; /* dtype: MLORA_FP32, MLORA_BF16 or MLORA_FP16 */
+  int32_t num_rows, vocab, dtype; /* 1 <= vocab <= MLORA_LOGITS_MAX_VOCAB; dtype: MLORA_FP32, MLORA_BF16 or MLORA_FP16 */
   int32_t num_requests;
   const void *logits;
   void *out;

@@ -43,3 +43,10 @@ def test_a_history_that_is_part_of_a_wider_matrix(L, host_tensors, rows, first):
 def test_history_lengths_are_refused(L, kw):  # noqa: F811
     s = made(m.mlora_logits, LOGITS, kw)
     assert L.lora_logits_adjust(ctypes.byref(s), None, None) == m.ERR_SHAPE
+
+
+@pytest.mark.parametrize("vocab", [2 ** 31 - 1, 2 ** 31 - 4096, 2 ** 31 - 65536])
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+def test_vocabularies_whose_last_slice_passes_31_bits_are_refused(L, vocab, dtype):  # noqa: F811
+    s = made(m.mlora_logits, LOGITS, dict(vocab=vocab, dtype=dtype, ld=1 << 31, ldo=1 << 31, mask_stride=1 << 26))
+    assert L.lora_logits_adjust(ctypes.byref(s), None, None) == m.ERR_SHAPE

@@ -11,6 +11,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "serve.cuh"
 
 namespace mlora {
@@ -152,9 +154,9 @@ cudaError_t launch_kv_append(const mlora_kv_cache &c, const mlora_kv_rows &r, in
   p.page = fast_div(c.page_tokens);
   p.slots = (int64_t)c.num_pages * c.page_tokens;
   p.per_row = fast_div((r.num_q_heads + c.num_kv_heads) * p.per_head.d + c.num_kv_heads * chunks);
-  for (int32_t row0 = 0; row0 < r.num_rows; row0 += 65535) {
+  for (int64_t row0 = 0; row0 < r.num_rows; row0 += 65535) {  // (the last step may pass 2^31)
     AppendParams q = p;
-    q.r.num_rows = min(65535, r.num_rows - row0);
+    q.r.num_rows = (int32_t)std::min<int64_t>(65535, r.num_rows - row0);
     q.r.cache_slot += row0;
     if (q.r.position) q.r.position += row0;
     q.r.k = static_cast<const uint16_t *>(r.k) + row0 * r.ldk;

@@ -1132,9 +1132,9 @@ cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a,
   const int64_t row_tiles = ((int64_t)a.max_pages * c.page_tokens / 16 + 3) * c.num_kv_heads * p.chunks;
   const int32_t step = (int32_t)std::min<int64_t>(kRowsPerLaunch, INT32_MAX / row_tiles);
   if (step < 1) return cudaErrorInvalidValue;  // (refused before: kv_attention_fits)
-  for (int32_t row0 = 0; row0 < a.num_rows; row0 += step) {
-    p.row0 = row0;
-    p.rows = std::min(step, a.num_rows - row0);
+  for (int64_t row0 = 0; row0 < a.num_rows; row0 += step) {  // (the last step may pass 2^31)
+    p.row0 = (int32_t)row0;
+    p.rows = (int32_t)std::min<int64_t>(step, a.num_rows - row0);
     const cudaError_t e = c.dtype == MLORA_BF16 ? dispatch<MLORA_BF16>(p, status, stream)
                                                 : dispatch<MLORA_FP16>(p, status, stream);
     if (e != cudaSuccess) return e;

@@ -314,9 +314,9 @@ cudaError_t launch(const mlora_logits &a, int32_t *status, cudaStream_t stream) 
   constexpr int kSlice = kThreads * (G ? G * kGroup : 1) * Vec<DT>::N;
   // a row may start up to one vector's elements after an aligned address
   const int64_t slices = ((int64_t)a.vocab + Vec<DT>::N - 1 + kSlice - 1) / kSlice;
-  for (int32_t row0 = 0; row0 < a.num_rows; row0 += 65535) {
-    const dim3 grid((unsigned)slices, (unsigned)min(65535, a.num_rows - row0));
-    const cudaError_t e = launch_waiting(logits_kernel<DT, G>, grid, dim3(kThreads), 0, 1, stream, a, row0, status);
+  for (int64_t row0 = 0; row0 < a.num_rows; row0 += 65535) {  // (the last step may pass 2^31)
+    const dim3 grid((unsigned)slices, (unsigned)std::min<int64_t>(65535, a.num_rows - row0));
+    const cudaError_t e = launch_waiting(logits_kernel<DT, G>, grid, dim3(kThreads), 0, 1, stream, a, (int32_t)row0, status);
     if (e != cudaSuccess) return e;
     api_count_launch();
   }

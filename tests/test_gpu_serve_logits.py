@@ -245,3 +245,12 @@ def test_history_in_a_column_view(dev, first, alone):
         keep = [0, 2, 3, 4]
         ref.assert_within(out.cpu()[keep], want[keep], tol[keep], "logits")
         assert int(st.item()) == m.STATUS_BAD_LENGTH and (out[1] == 55).all()
+
+
+def test_as_many_rows_as_are_counted(dev):
+    """2^31 - 1 rows: the launches' first rows end below 2^31."""
+    rows = 2 ** 31 - 1
+    x = torch.arange(4096, dtype=torch.float16, device=dev).repeat((rows + 4095) // 4096)[:rows, None]
+    out = torch.empty_like(x)
+    m.lora_logits_adjust(out, x)
+    assert torch.equal(out, x)

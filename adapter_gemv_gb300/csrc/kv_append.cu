@@ -81,8 +81,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     pos[i] = row < r.num_rows && r.rotary_dim ? r.position[row] : 0;
   }
   uint4 x[ROWS], y[ROWS];
+  // Rows without a slot are loaded, too (the arrays have them): their slot is on its way. Waiting for it before the
+  // loads: 164 us instead of 132 for 12604 rows, 29 instead of 24 for 2000; a row a thread, eight one after another
+  // with the next slot fetched ahead: 136 and 28.
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {  // (rows without a slot are read, too: their slot is not known yet)
+  for (int i = 0; i < ROWS; ++i) {
     if (row0 + i >= r.num_rows) continue;
     x[i] = ldg_u4(src + (row0 + i) * ld);
     if (pairs) y[i] = ldg_u4(src + (row0 + i) * ld + half);

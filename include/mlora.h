@@ -367,7 +367,8 @@ typedef struct {
  *   (a, b) = elements (m, m + rotary_dim/2) of a head, or (2m, 2m+1) with rope_interleaved;
  * the elements from rotary_dim on, and all of them without tables (rope_cos = NULL), are copied.
  * Two rows with the same cache slot leave either's values there. q_out may be q. Rows are
- * ldk, ldv, ldq, ldq_out elements apart (multiples of 8; pointers 16-byte aligned).
+ * ldk, ldv, ldq, ldq_out elements apart (multiples of 8; pointers 16-byte aligned). All num_rows rows of k, v and q have to
+ * be there: those of rows without a slot are loaded with the others, before the slots are known, and not used.
  * Skipped rows, with their status: a slot < -1 or >= num_pages * page_tokens (BAD_SLOT), a position
  * outside [0, max_position) where there are tables (BAD_LENGTH). */
 typedef struct {

@@ -50,6 +50,11 @@ int check_rows(const void *p, int64_t ld, int64_t width) {
   return MLORA_OK;
 }
 
+// In place, a row's output has to be where its input is: with other distances rows would overwrite each other's inputs.
+int check_in_place(const void *in, const void *out, int64_t ld_in, int64_t ld_out, int32_t rows) {
+  return in == out && ld_in != ld_out && rows > 1 ? MLORA_ERR_SHAPE : MLORA_OK;
+}
+
 int check_table(int32_t max_pages, int64_t table_stride, int32_t page_tokens) {
   if (max_pages < 0 || table_stride < max_pages) return MLORA_ERR_SHAPE;
   if ((int64_t)max_pages * page_tokens > INT32_MAX) return MLORA_ERR_SHAPE;  // positions are int32
@@ -100,6 +105,7 @@ int lora_kv_append(const mlora_kv_cache *cache, const mlora_kv_rows *r, int32_t 
   if (r->num_q_heads) {
     TRY(check_rows(r->q, r->ldq, qwidth));
     TRY(check_rows(r->q_out, r->ldq_out, qwidth));
+    TRY(check_in_place(r->q, r->q_out, r->ldq, r->ldq_out, r->num_rows));
   }
   if (!aligned(r->cache_slot, 8) || !all_aligned(4, r->position, dev_status)) return MLORA_ERR_ALIGN;
   return done(mlora::launch_kv_append(*cache, *r, layer, dev_status, static_cast<cudaStream_t>(stream)),
@@ -123,6 +129,7 @@ int lora_kv_attention(const mlora_kv_cache *cache, const mlora_kv_attn *a, int32
   const int64_t width = (int64_t)a->num_q_heads * cache->head_dim;
   TRY(check_rows(a->q, a->ldq, width));
   TRY(check_rows(a->out, a->ldo, width));
+  TRY(check_in_place(a->q, a->out, a->ldq, a->ldo, a->num_rows));
   if (!a->position || (a->num_requests && a->max_pages && !a->page_table)) return MLORA_ERR_NULL;
   if (!all_aligned(4, a->position, a->row_request, a->page_table, a->lse, dev_status)) return MLORA_ERR_ALIGN;
   const int64_t need = lora_kv_attention_workspace(cache, a->num_q_heads);
@@ -140,6 +147,7 @@ int lora_logits_adjust(const mlora_logits *a, int32_t *dev_status, void *stream)
   if (a->num_rows == 0) return MLORA_OK;
   if (!a->logits || !a->out) return MLORA_ERR_NULL;
   if (a->ld < a->vocab || a->ldo < a->vocab) return MLORA_ERR_SHAPE;
+  TRY(check_in_place(a->logits, a->out, a->ld, a->ldo, a->num_rows));
   // an empty array may be NULL beside its lengths
   if (!a->prompt_len != !a->total_len || (a->tokens && !a->total_len)) return MLORA_ERR_NULL;
   if (a->total_len && a->tokens_stride > 0 && !a->tokens) return MLORA_ERR_NULL;

@@ -289,6 +289,8 @@ MLORA_API int lora_sgmv_sequence(const mlora_group *groups, int32_t num_groups, 
  *     device memory, so a captured graph can be replayed). num_rows is the capacity of the row
  *     arrays; a row that stands for nothing has -1 as its request, position and cache slot, and no
  *     call reads or writes anything for it but where said.
+ *   - Where an output may be an input (said at the call), its rows are as far apart as the input's. Outputs overlap inputs
+ *     in no other way.
  *   - Every kernel waits for the work before it in the stream before it reads or writes any memory,
  *     whether or not it was launched programmatically. lora_kv_layout writes the segments that the adapters' calls
  *     read before such a wait: the first of them after it is launched without MLORA_LAUNCH_PROGRAMMATIC. */
@@ -396,7 +398,7 @@ MLORA_API int lora_kv_append(const mlora_kv_cache *cache, const mlora_kv_rows *r
  * continuation, the rows of a prompt) are rows of their own. Cache contents outside the tokens that a
  * row sees, NaN included, do not reach its output. An element of V that is an infinity makes the output's that infinity,
  * however small the token's weight; a NaN, or infinities of both signs, make it NaN. A row whose every score is -inf has
- * no weights: its output is 0 and its lse -inf. The long rows' tokens are split over the whole GPU
+ * no weights: its output is 0 and its lse -inf. out may be q. The long rows' tokens are split over the whole GPU
  * and joined in a fixed order: the same call gives the same bits.
  * workspace: lora_kv_attention_workspace bytes of device memory, 16-byte aligned, zeroed by the
  * caller before its first use; every call leaves the part that has to be zero at zero. Calls that may

@@ -370,3 +370,16 @@ def test_a_value_that_only_later_rows_see(dev, hq, hk, d, pt, dtype, window):
     hit = hit[:, None, :].expand(-1, hq, -1)
     assert not torch.isfinite(out[hit]).any()
     ref.assert_within(out[~hit], want[~hit], tol[~hit], "out")
+
+
+@pytest.mark.parametrize("lens, per, hq, hk, d", [([5, 9000, 40], 1, 8, 1, 128), ([300] * 40, 3, 15, 5, 80), ([70], 1, 40, 2, 64)])
+def test_in_place(dev, lens, per, hq, hk, d):
+    """out may be q: rows that are whole, split over the GPU, share tiles, or have more heads than a tile."""
+    c = Case(dev, lens, hq, hk, d, per=per)
+    c.run()
+    want = c.out.clone()
+    q = c.q.clone()
+    call = m.KvAttention(q, q, c.cache, c.table, c.position, c.layer, c.workspace, row_request=c.request, lse=c.lse,
+                         scale=c.scale)
+    call()
+    assert torch.equal(q, want)

@@ -7,7 +7,7 @@ import torch
 
 import adapter_gemv_gb300 as m
 from adapter_gemv_gb300 import serve
-from test_serve_abi import LOGITS, L, made  # noqa: F401
+from test_serve_abi import ATTN, CACHE, LOGITS, ROWS, L, made  # noqa: F401
 
 
 @pytest.fixture
@@ -50,3 +50,14 @@ def test_history_lengths_are_refused(L, kw):  # noqa: F811
 def test_vocabularies_whose_last_slice_passes_31_bits_are_refused(L, vocab, dtype):  # noqa: F811
     s = made(m.mlora_logits, LOGITS, dict(vocab=vocab, dtype=dtype, ld=1 << 31, ldo=1 << 31, mask_stride=1 << 26))
     assert L.lora_logits_adjust(ctypes.byref(s), None, None) == m.ERR_SHAPE
+
+
+def test_in_place_rows_of_another_distance_are_refused(L):  # noqa: F811
+    """out = in with rows further apart: a row's output would lie over other rows' inputs."""
+    c = made(m.mlora_kv_cache, CACHE, {})
+    for kw in (dict(ldo=104), dict(ld=104)):
+        assert L.lora_logits_adjust(ctypes.byref(made(m.mlora_logits, LOGITS, kw)), None, None) == m.ERR_SHAPE
+    for kw in (dict(ldq_out=520), dict(ldq=520)):
+        assert L.lora_kv_append(ctypes.byref(c), ctypes.byref(made(m.mlora_kv_rows, ROWS, kw)), 1, None, None) == m.ERR_SHAPE
+    for kw in (dict(ldo=520), dict(ldq=520)):
+        assert L.lora_kv_attention(ctypes.byref(c), ctypes.byref(made(m.mlora_kv_attn, ATTN, kw)), 1, None, None) == m.ERR_SHAPE

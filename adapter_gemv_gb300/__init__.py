@@ -333,5 +333,5 @@ def abi_version() -> int:
 from .serve import (  # noqa: E402
     ERR_WORKSPACE, KV_MAX_HEAD_DIM, KV_MAX_REQUESTS, MLORA_FP32, STATUS_BAD_LENGTH, STATUS_BAD_REQUEST,
     STATUS_BAD_TOKEN, STATUS_NO_PAGES, KvAppend, KvAttention, KvBatch, KvCache, LogitsAdjust, Rope,
-    kv_attention_workspace, lora_kv_append, lora_kv_attention, lora_kv_attention_workspace, lora_kv_layout,
-    lora_logits_adjust, make_kv_cache, mlora_kv_attn, mlora_kv_batch, mlora_kv_cache, mlora_kv_rows, mlora_logits)
+    kv_attention_workspace, lora_kv_append, lora_kv_attention, lora_kv_attention_ex, lora_kv_attention_workspace,
+    lora_kv_layout, lora_logits_adjust, make_kv_cache, mlora_kv_attn, mlora_kv_batch, mlora_kv_cache, mlora_kv_rows, mlora_logits)

@@ -55,7 +55,9 @@ constexpr int kMaxGroup = 16;        // query heads of a work item
 constexpr int kFewTiles = 16;
 // Rows of one request share a tile's columns, `group` each, where the SMs have at least kShare8 (row, key-value head)s
 // each: up to 8 columns, which costs masks and 1.2 us for the list. From kShare16 on up to 16, twice the products
-// and longer joins, if a request's rows (their average) need them. Measured (us), 8 heads of 128, 500 to 1500 tokens
+// and longer joins, if a request's rows need them: their number is the caller's to say (the host sees capacities only; 40
+// requests of 5 rows, groups of 4, in a page table of 256 places: 82 us by the capacities, 58 told; 200 decoding rows padded
+// to 256, groups of 8: 130 and 125; a prompt of 200 in that table 18.1 and 17.4). Measured (us), 8 heads of 128, 500 to 1500 tokens
 // unless said; a row to a tile, 8 columns, 16 columns:
 //   group 4: 4 requests x 4 rows (0.8 an SM) 15.3  17.6  22.9;  8 x 4 (1.7) 22.6  18.8  24.2;  64 x 2 (6.7) 71.7  49.9  52.2;
 //     32 x 4 (6.7) 55.1  39.7  38.9;  64 x 5 (17) 142  98  83;  16 x 64 (54) 305  189  137;
@@ -1111,8 +1113,8 @@ int64_t kv_attention_workspace_bytes(int32_t head_dim) {
   return (int64_t)kCounterBytes + (int64_t)attn_ctas() * kPartialSlots * partial_floats(dp) * sizeof(float);
 }
 
-cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a, int32_t layer, int32_t *status,
-                                cudaStream_t stream) {
+cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a, int32_t layer, int32_t rows_per_request,
+                                int32_t *status, cudaStream_t stream) {
   AttnParams p{};
   p.c = c;
   p.a = a;
@@ -1122,8 +1124,12 @@ cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a,
   p.group = a.num_q_heads / c.num_kv_heads;
   p.chunks = (p.group + kMaxGroup - 1) / kMaxGroup;
   const int64_t per_sm = a.num_rows * (int64_t)c.num_kv_heads / attn_ctas();
-  const int columns = per_sm >= kShare16 && a.num_rows > a.num_requests * (int64_t)(8 / p.group) ? 16 : 8;
-  p.pack = a.row_request && a.num_rows > a.num_requests && per_sm >= kShare8 ? std::max(1, columns / p.group) : 1;
+  // rows of a request: what the caller says (the most), or as many as the arrays have place for on average
+  const int64_t most = rows_per_request ? rows_per_request
+                                        : (a.num_rows + (int64_t)a.num_requests - 1) / std::max(1, a.num_requests);
+  const int columns = per_sm >= kShare16 && most > 8 / p.group ? 16 : 8;
+  p.pack = a.row_request && most > 1 && per_sm >= kShare8 ? std::max(1, columns / p.group) : 1;
+  if (rows_per_request) p.pack = std::min(p.pack, rows_per_request);
   p.by_group = fast_div(p.group);
   p.scale_log2 = a.scale * 1.44269504088896340736f;
   p.counters = static_cast<int32_t *>(a.workspace);

@@ -16,8 +16,8 @@ void api_count_launch();
 cudaError_t launch_kv_layout(const mlora_kv_batch &b, int32_t *status, cudaStream_t stream);
 cudaError_t launch_kv_append(const mlora_kv_cache &c, const mlora_kv_rows &r, int32_t layer, int32_t *status,
                              cudaStream_t stream);
-cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a, int32_t layer, int32_t *status,
-                                cudaStream_t stream);
+cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a, int32_t layer, int32_t rows_per_request,
+                                int32_t *status, cudaStream_t stream);
 bool kv_attention_fits(const mlora_kv_cache &c, const mlora_kv_attn &a);  // one row's tiles counted in 31 bits
 int64_t kv_attention_workspace_bytes(int32_t head_dim);
 cudaError_t launch_logits_adjust(const mlora_logits &a, int32_t *status, cudaStream_t stream);

@@ -119,9 +119,14 @@ int64_t lora_kv_attention_workspace(const mlora_kv_cache *cache, int32_t num_q_h
 
 int lora_kv_attention(const mlora_kv_cache *cache, const mlora_kv_attn *a, int32_t layer, int32_t *dev_status,
                       void *stream) {
+  return lora_kv_attention_ex(cache, a, layer, 0, dev_status, stream);
+}
+
+int lora_kv_attention_ex(const mlora_kv_cache *cache, const mlora_kv_attn *a, int32_t layer, int32_t rows_per_request,
+                         int32_t *dev_status, void *stream) {
   if (!a) return MLORA_ERR_NULL;
   TRY(check_cache(cache, layer));
-  if (a->num_rows < 0 || a->num_requests < 0 || a->window < 0) return MLORA_ERR_SHAPE;
+  if (rows_per_request < 0 || a->num_rows < 0 || a->num_requests < 0 || a->window < 0) return MLORA_ERR_SHAPE;
   if (a->num_q_heads < 1 || a->num_q_heads % cache->num_kv_heads || !std::isfinite(a->scale)) return MLORA_ERR_SHAPE;
   TRY(check_table(a->max_pages, a->table_stride, cache->page_tokens));
   if (!mlora::kv_attention_fits(*cache, *a)) return MLORA_ERR_SHAPE;
@@ -136,7 +141,7 @@ int lora_kv_attention(const mlora_kv_cache *cache, const mlora_kv_attn *a, int32
   if (need && !a->workspace) return MLORA_ERR_NULL;
   if (!aligned(a->workspace, 16)) return MLORA_ERR_ALIGN;
   if (a->workspace_bytes < need) return MLORA_ERR_WORKSPACE;
-  return done(mlora::launch_kv_attention(*cache, *a, layer, dev_status, static_cast<cudaStream_t>(stream)),
+  return done(mlora::launch_kv_attention(*cache, *a, layer, rows_per_request, dev_status, static_cast<cudaStream_t>(stream)),
               "cache attention launch");
 }
 

@@ -68,6 +68,7 @@ SIGNATURES.update({
     "lora_kv_layout": [ctypes.POINTER(mlora_kv_batch), _V, _V],
     "lora_kv_append": [_PC, ctypes.POINTER(mlora_kv_rows), _I, _V, _V],
     "lora_kv_attention": [_PC, ctypes.POINTER(mlora_kv_attn), _I, _V, _V],
+    "lora_kv_attention_ex": [_PC, ctypes.POINTER(mlora_kv_attn), _I, _I, _V, _V],
     "lora_logits_adjust": [ctypes.POINTER(mlora_logits), _V, _V],
 })
 
@@ -220,10 +221,11 @@ def kv_attention_workspace(cache, num_q_heads: int) -> torch.Tensor:
 
 class KvAttention:
     """A prepared lora_kv_attention call. Row i of q and out is a token of request row_request[i] (default:
-    request i) that sees the cached tokens 0 .. position[i], the last `window` of them if window > 0."""
+    request i) that sees the cached tokens 0 .. position[i], the last `window` of them if window > 0. rows_per_request: how
+    many rows a request has at most (1: a decode step), 0 if that is not known; it decides the time only."""
 
     def __init__(self, out, q, cache, page_table, position, layer: int, workspace, row_request=None, lse=None,
-                 scale: Optional[float] = None, window: int = 0, status=None):
+                 scale: Optional[float] = None, window: int = 0, status=None, rows_per_request: int = 0):
         c = self.cache = make_kv_cache(cache)
         n, d = int(position.numel()), c.struct.head_dim
         if q.shape[1] % d:
@@ -245,16 +247,23 @@ class KvAttention:
             s.lse = _dev(lse, "lse", torch.float32)
         s.workspace, s.workspace_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
         self.ref, self.layer, self.status = ctypes.pointer(s), int(layer), _i32(status, "status")
-        self.fn = lib().lora_kv_attention
+        self.fn, self.rows_per_request = lib().lora_kv_attention_ex, int(rows_per_request)
 
     def __call__(self, stream=None):
-        _check(self.fn(self.cache.ref, self.ref, self.layer, self.status, _stream(stream)))
+        _check(self.fn(self.cache.ref, self.ref, self.layer, self.rows_per_request, self.status, _stream(stream)))
 
 
 def lora_kv_attention(out, q, cache, page_table, position, layer, workspace, row_request=None, lse=None, scale=None,
                       window=0, status=None, stream=None) -> None:
     """Attention of rows q (columns: query heads x head_dim) over the paged cache, into out."""
     KvAttention(out, q, cache, page_table, position, layer, workspace, row_request, lse, scale, window, status)(stream)
+
+
+def lora_kv_attention_ex(out, q, cache, page_table, position, layer, workspace, rows_per_request, row_request=None,
+                         lse=None, scale=None, window=0, status=None, stream=None) -> None:
+    """The same, told how many rows a request has at most."""
+    KvAttention(out, q, cache, page_table, position, layer, workspace, row_request, lse, scale, window, status,
+                rows_per_request)(stream)
 
 
 class LogitsAdjust:

@@ -116,7 +116,7 @@ class Server:
         at = batch.position.long()
         x = self.model.embed[self.tokens[batch.row_request.long(), at].long()]
         for layer in range(c.layers):
-            x = self._layer(layer, x, batch)
+            x = self._layer(layer, x, batch, max(new))
         last = (batch.seg_offsets[1:self.places + 1] - 1).clamp(min=0).long()
         logits = torch.matmul(norm(x)[last], self.model.head).float()
         ran = torch.tensor([i if n > 0 else -1 for i, n in enumerate(new)], dtype=torch.int32, device=self.dev)
@@ -140,13 +140,13 @@ class Server:
                             batch.seg_slot, self.status)
         return ys
 
-    def _layer(self, layer, x, batch):
+    def _layer(self, layer, x, batch, rows_per_request):
         q, k, v = self._project(("q", "k", "v"), norm(x), layer, batch)
         m.lora_kv_append(self.cache, k, v, batch.cache_slot, layer, q=q, position=batch.position, rope=self.model.rope,
                          status=self.status)
         out = torch.empty_like(q)
-        m.lora_kv_attention(out, q, self.cache, self.page_table, batch.position, layer, self.workspace,
-                            row_request=batch.row_request, status=self.status)
+        m.lora_kv_attention_ex(out, q, self.cache, self.page_table, batch.position, layer, self.workspace, rows_per_request,
+                               row_request=batch.row_request, status=self.status)
         x = x + self._project(("o",), out, layer, batch)[0]
         gate, up = self._project(("gate", "up"), norm(x), layer, batch)
         return x + self._project(("down",), torch.nn.functional.silu(gate) * up, layer, batch)[0]

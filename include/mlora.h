@@ -428,6 +428,12 @@ typedef struct {
 MLORA_API int64_t lora_kv_attention_workspace(const mlora_kv_cache *cache, int32_t num_q_heads);
 MLORA_API int lora_kv_attention(const mlora_kv_cache *cache, const mlora_kv_attn *args, int32_t layer,
                                 int32_t *dev_status, void *stream);
+/* The same, told how many rows a request has at most in this call (1: a decode step; a prompt's or a draft's length; 0: not
+ * known). It decides how many rows are taken through the cache together, which changes the time and the rounding, not
+ * what is computed; a wrong number is only slower. Without it the call goes by num_rows / num_requests, which says little where
+ * the rows are padded or the page table has places without a request. */
+MLORA_API int lora_kv_attention_ex(const mlora_kv_cache *cache, const mlora_kv_attn *args, int32_t layer,
+                                   int32_t rows_per_request, int32_t *dev_status, void *stream);
 
 /* lora_logits_adjust: out[i][t] from logits[i][t], for row i of request r = row_request[i] (-1: the row's
  * output is left untouched), in fp32 and rounded once to the logits' type. With the request's history

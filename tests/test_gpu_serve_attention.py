@@ -383,3 +383,20 @@ def test_in_place(dev, lens, per, hq, hk, d):
                          scale=c.scale)
     call()
     assert torch.equal(q, want)
+
+
+@pytest.mark.parametrize("hq, hk, d", [(8, 8, 128), (15, 5, 80), (64, 16, 64), (16, 2, 256), (40, 2, 64)])
+@pytest.mark.parametrize("rows_per_request", [0, 1, 2, 3, 7, 2 ** 31 - 1])
+def test_rows_per_request_changes_no_result(dev, hq, hk, d, rows_per_request):
+    """Right or wrong, a request's number of rows decides what shares a tile only: drafts of 1 to 6 rows and padding in a
+    table with more places than requests, few rows and many."""
+    lens = [300, 17, 64, 1, 150]
+    for times in (1, 40):
+        c = Case(dev, lens + [5] * 300, hq, hk, d, layers=1)
+        rows = []
+        for r, n in enumerate(lens):
+            rows += [(r, p) for p in range(max(0, n - r - 2), n)]
+        with_rows(c, (rows + [(-1, -1)] * 9) * times, torch.Generator(device=dev).manual_seed(13))
+        c.run(rows_per_request=rows_per_request)
+        assert int(c.status.item()) == 0
+        c.check()

@@ -61,3 +61,10 @@ def test_in_place_rows_of_another_distance_are_refused(L):  # noqa: F811
         assert L.lora_kv_append(ctypes.byref(c), ctypes.byref(made(m.mlora_kv_rows, ROWS, kw)), 1, None, None) == m.ERR_SHAPE
     for kw in (dict(ldo=520), dict(ldq=520)):
         assert L.lora_kv_attention(ctypes.byref(c), ctypes.byref(made(m.mlora_kv_attn, ATTN, kw)), 1, None, None) == m.ERR_SHAPE
+
+
+def test_a_negative_number_of_rows_per_request_is_refused(L):  # noqa: F811
+    c, a = made(m.mlora_kv_cache, CACHE, {}), made(m.mlora_kv_attn, ATTN, dict(num_rows=0))
+    assert L.lora_kv_attention_ex(ctypes.byref(c), ctypes.byref(a), 1, -1, None, None) == m.ERR_SHAPE
+    for rows in (0, 1, 9, 2 ** 31 - 1):
+        assert L.lora_kv_attention_ex(ctypes.byref(c), ctypes.byref(a), 1, rows, None, None) == 0

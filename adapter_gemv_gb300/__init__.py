@@ -128,9 +128,15 @@ def _rows(t: torch.Tensor, what: str, dtype) -> int:
     return t.stride(0)
 
 
+# The current stream's handle without making a Stream object (2.8 us of a call), where torch offers it: a private call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
-    if stream is None:  # the current stream's handle, without making a Stream object (2.8 us of a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

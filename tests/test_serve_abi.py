@@ -178,3 +178,25 @@ def test_layout_reference_by_hand():
     assert got["seg_offsets"] == [0, 3, 3, 4, 6] and got["seg_slot"] == [5, 6, 7, -1]
     assert got["row_request"] == [0, 0, 0, 2, -1, -1] and got["position"] == [2, 3, 4, 4, -1, -1]
     assert got["cache_slot"] == [30, 31, 16, 12, -1, -1] and got["row_slot"] == [5, 5, 5, 7, -1, -1]
+
+
+def test_the_current_stream_with_and_without_torchs_private_call(monkeypatch):
+    import types
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=77))
+    monkeypatch.setattr(m, "_raw_stream", lambda device: 1000 + device)
+    assert m._stream(None) == 1003
+    monkeypatch.setattr(m, "_raw_stream", None)
+    assert m._stream(None) == 77
+    assert m._stream(types.SimpleNamespace(cuda_stream=5)) == 5 and m._stream(9) == 9
+
+
+def test_the_package_imports_without_torchs_private_call():
+    import subprocess
+    import sys
+    code = ("import torch; hasattr(torch._C, '_cuda_getCurrentRawStream') and delattr(torch._C, '_cuda_getCurrentRawStream')\n"
+            "import types; torch.cuda.current_stream = lambda: types.SimpleNamespace(cuda_stream=77)\n"
+            "torch.cuda.current_device = lambda: 0\n"
+            "import adapter_gemv_gb300 as m; assert m._stream(None) == 77")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root)

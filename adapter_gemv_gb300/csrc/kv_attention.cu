@@ -25,8 +25,13 @@
 //     as rows, half of every product is padding, and the accumulators twice as many.)
 //   * The maximum is not followed exactly: m moves when a score passes it by 2^kSlack, which one vote
 //     per tile decides; weights up to 2^kSlack are as exact as those up to 1.
-//   * The weights are rounded to 16 bits for the second product. Their remainder, rounded likewise, goes
-//     through a second one, so what is left is fp32's error; the products cost nothing (above).
+//   * The weights are rounded to the cache's type for the second product. Their remainder, rounded likewise, goes
+//     through a second one: 16 significant bits of a weight with bf16, 22 with fp16 (it is off by 2^-16, 2^-22 of itself
+//     at most), against the output's 8 and 11. Of 256 requests of up to 4096 tokens one output in 360 is rounded to the
+//     other side than the plain form's in fp32 (of which one in 2100 is not the exact value's), and the error against 64
+//     bits is the same. A third part would hold fp32's bits: the same time where memory bounds (256 requests), 5 % more
+//     for 8 requests of 1000 tokens, 8 % for prompt rows, 12 % for those at 256 elements a head. The sums are the matrix
+//     instructions' fp32 accumulators, the exponential is ex2.approx (2 ulp).
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -44,25 +49,33 @@ namespace {
 // (64 rows of 8 x 64 elements: 41.9 us with 16, 39.8 with 32).
 constexpr int tile_tokens(int dp) { return dp == 64 ? 32 : 16; }
 constexpr int kRowsPerLaunch = 1024;
-constexpr int kMinTiles = 2;         // a warp's share of a small call, so that few pieces have to be joined
-// A CTA's boundary inside a (row, head) of at most this many tiles moves to its nearer end, where the CTAs'
-// shares are at most kSmallShare tiles (above).
+// A warp's share of a small call, so that few pieces have to be joined: with 1, 2, 4 tiles, 61 tokens 6.1, 6.4, 7.0 us, 4
+// requests of 4 rows 15.5, 15.2, -, 8 rows of 131071 tokens 354, 331, -; the others alike.
+constexpr int kMinTiles = 2;
+// A CTA's boundary inside a (row, head) of at most kWhole tiles moves to its nearer end, where the CTAs' shares are at
+// most kSmallShare tiles, and of at most kWholeLarge where they are larger. Measured (us):
+//   kWhole 0, 96, 400: 61 tokens 9.1  6.4  6.5;  300 tokens 11.0  8.8  8.8;  8 requests of 4 rows 20.3  18.7  18.8;  16 requests
+//     of 100 to 2000 tokens 19.8  18.6  19.0
+//   kWholeLarge 0, 24, 96, 150: 197 short requests of 3 rows 39.7  37.0  34.7  34.8;  64 requests, heads of 64: 41.1  40.2  39.1
+//     42.0;  32 requests x 4 rows -  39.4  41.7  41.5;  the same with groups of 8 -  51.1  52.4  52.5;  64 at pages of 1 token
+//     -  64.6  66.0  72.5;  32 long requests 81.0  79.8  78.3  79.5
 constexpr int kSmallShare = 64, kWhole = 96, kWholeLarge = 24;
 constexpr int kMaxGroup = 16;        // query heads of a work item
 // Where a warp has at most this many tiles, the list holds an empty one behind every (row, head): what starting
 // and ending one costs, about a tile's products (0.5 us), counts beside the tiles then, not in a call that
-// waits for memory.
+// waits for memory. Never, at 16, always: 197 requests of 3 rows 45.5  37.0  37.1 us, 37 of 3 rows with a window 24.9  23.0
+// 23.0, 256 long requests 210.3  210.0  211.0.
 constexpr int kFewTiles = 16;
 // Rows of one request share a tile's columns, `group` each, where the SMs have at least kShare8 (row, key-value head)s
 // each: up to 8 columns, which costs masks and 1.2 us for the list. From kShare16 on up to 16, twice the products
-// and longer joins, if a request's rows need them: their number is the caller's to say (the host sees capacities only; 40
-// requests of 5 rows, groups of 4, in a page table of 256 places: 82 us by the capacities, 58 told; 200 decoding rows padded
-// to 256, groups of 8: 130 and 125; a prompt of 200 in that table 18.1 and 17.4). Measured (us), 8 heads of 128, 500 to 1500 tokens
-// unless said; a row to a tile, 8 columns, 16 columns:
+// and longer joins, if a request's rows need them: their number is the caller's to say (the host sees capacities only:
+// 40 requests of 5 rows, groups of 4, in a page table of 256 places 82 us by the capacities, 58 told; 200 decoding rows
+// padded to 256, groups of 8, 130 and 125; a prompt of 200 in that table 18.1 and 17.4). Measured (us), 8 heads of 128,
+// 500 to 1500 tokens unless said; a row to a tile, 8 columns, 16 columns:
 //   group 4: 4 requests x 4 rows (0.8 an SM) 15.3  17.6  22.9;  8 x 4 (1.7) 22.6  18.8  24.2;  64 x 2 (6.7) 71.7  49.9  52.2;
-//     32 x 4 (6.7) 55.1  39.7  38.9;  64 x 5 (17) 142  98  83;  16 x 64 (54) 305  189  137;
-//     a prompt of 256 (13) 23.1  18.6  19.0, of 1024 (54) 347  232  182
-//   group 1: 64 x 8 205  52  54    group 2: 64 x 8 207  75  59    group 8: 32 x 4 (6.7) 55.9  -  50.6
+//     32 x 4 (6.7) 55.1  39.7  39.4;  64 x 5 (17) 142  98  83;  16 x 64 (54) 305  189  138;
+//     a prompt of 256 (13) 23.1  18.6  19.3, of 1024 (54) 347  232  186
+//   group 1: 64 x 8 205  52  54    group 2: 64 x 8 207  75  59    group 8: 32 x 4 (6.7) 55.9  -  51.1
 //   group 3, 37 x 3 short ones (3.6) 25.0  23.0  25.6
 constexpr int kShare8 = 1, kShare16 = 6;
 constexpr float kSlack = 8.f;        // log2 of how far a weight may pass 1 before m moves

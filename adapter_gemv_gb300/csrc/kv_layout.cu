@@ -179,7 +179,8 @@ cudaError_t launch_kv_layout(const mlora_kv_batch &b, int32_t *status, cudaStrea
   };
   // Rows and requests, of which most have an entry. Measured: 32 decoding requests 3.3 us with one CTA of 256
   // threads, 3.9 with a cluster of eight; 67 requests and 2770 rows 9.8 and 4.2; 4096 requests and 48
-  // thousand rows 20 with the cluster, 9.4 with a CTA per 1024 entries (11 per 512, 17 per 256).
+  // thousand rows 20 with the cluster, 9.4 with a CTA per 1024 entries (11 per 512, 17 per 256), and 15.8 in place, where the
+  // second launch has to follow.
   const int64_t work = (int64_t)b.num_rows + b.num_requests;
   if (work <= 512) return run(1, 256, kEntries | kState, 1);
   if (work <= 8 * 1024) return run(8, 512, kEntries | kState, 8);

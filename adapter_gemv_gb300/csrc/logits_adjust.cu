@@ -14,9 +14,14 @@
 // their count (occurrences past the prompt, whole-number atomics: the order does not matter; bit 31 for a
 // token of the prompt) and bias (the entry's number + 1, then its value, as one 64-bit maximum: of several
 // with one id the last wins) in arrays by that number; more than kPlaces of them, of a long history, take
-// several turns. Each CTA of a row reads the whole history: at most some 16 KB, from L2 after the first.
+// several turns. Each CTA of a row reads the whole history and list, from L2 after the first: once for the bits and
+// once more for every kPlaces tokens that it finds in its slice. That is some 16 KB twice for a history of 4096, but it
+// grows with the history times the touched tokens of a slice, and the choice of the slices does not look at it. At 128001
+// fp32 logits a row with histories of 1, 4096, 32768, 131072 tokens: one row 3.5, 5.8, 25, 154 us; 64 rows 19, 23, 167,
+// 1255; 256 rows 50, 71, 567, 4726 (token ids by a power law).
 // Measured at 256 x 128001 fp32 with histories of 512 to 4096 tokens, lists of 300 and half the rows masked: 61 us,
-// 4.3 TB/s (43 us, 6.1 TB/s, without history, list and mask). What is left is the touched tokens' chain: bits
+// 4.3 TB/s (43 us, 6.1 TB/s, without history, list and mask), 101 us in place, where the bits come before the stream;
+// bf16 53 and 105. What is left is the touched tokens' chain: bits
 // 4 us, numbers 1, counts 8, their logits 4. Also tried there: a table entry for every token of the slice,
 // its logits held in registers until the counts were there, 88 us; the touched tokens adjusted in the stream, with
 // the counts before it, 75 to 82; a CTA's share as one long stretch, 76; a list of the slice's tokens in

@@ -393,7 +393,8 @@ MLORA_API int lora_kv_append(const mlora_kv_cache *cache, const mlora_kv_rows *r
  * token 0),
  *   w_t = exp(scale q[i][h] . K[t][h / G]) / sum of these,   out[i][h] = sum_t w_t V[t][h / G],
  *   lse[i][h] = log of that sum,   G = num_q_heads / num_kv_heads,
- * the scores, the sums and the softmax's statistics in fp32, the output rounded once. A row with
+ * the scores, the sums and the softmax's statistics in fp32 (accumulated by matrix instructions; a weight enters the second
+ * sum to 2^-16 of itself with bf16, 2^-22 with fp16), the output rounded once. A row with
  * position -1 sees nothing: its output is 0 and its lse -inf. Several rows of one request (a drafted
  * continuation, the rows of a prompt) are rows of their own. Cache contents outside the tokens that a
  * row sees, NaN included, do not reach its output. An element of V that is an infinity makes the output's that infinity,

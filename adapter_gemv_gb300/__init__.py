@@ -341,3 +341,6 @@ from .serve import (  # noqa: E402
     STATUS_BAD_TOKEN, STATUS_NO_PAGES, KvAppend, KvAttention, KvBatch, KvCache, LogitsAdjust, Rope,
     kv_attention_workspace, lora_kv_append, lora_kv_attention, lora_kv_attention_ex, lora_kv_attention_workspace,
     lora_kv_layout, lora_logits_adjust, make_kv_cache, mlora_kv_attn, mlora_kv_batch, mlora_kv_cache, mlora_kv_rows, mlora_logits)
+from .step import (  # noqa: E402
+    FP8_BLOCK, ROW_MAX_WIDTH, SAMPLE_MAX_VOCAB, Fp8Matmul, Quantize, RmsNorm, Sample, lora_fp8_matmul, lora_quantize,
+    lora_rms_norm, lora_sample, mlora_matmul, mlora_norm, mlora_quant, mlora_sampling)

@@ -1,5 +1,5 @@
 // serve.h -- launchers of the operators around the adapted projections (cache layout, append,
-// attention, logits), shared by serve_api.cu and the kernel files.
+// attention, logits; norm, 8-bit rows and products, sampling), shared by the C ABI files and the kernel files.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -21,6 +21,10 @@ cudaError_t launch_kv_attention(const mlora_kv_cache &c, const mlora_kv_attn &a,
 bool kv_attention_fits(const mlora_kv_cache &c, const mlora_kv_attn &a);  // one row's tiles counted in 31 bits
 int64_t kv_attention_workspace_bytes(int32_t head_dim);
 cudaError_t launch_logits_adjust(const mlora_logits &a, int32_t *status, cudaStream_t stream);
+cudaError_t launch_rms_norm(const mlora_norm &a, cudaStream_t stream);
+cudaError_t launch_quantize(const mlora_quant &a, cudaStream_t stream);
+cudaError_t launch_fp8_matmul(const mlora_matmul &a, int32_t *status, cudaStream_t stream);
+cudaError_t launch_sample(const mlora_sampling &a, int32_t *status, cudaStream_t stream);
 
 // Defined in decode_launch.cu: number of SMs of the current device.
 int sm_count();

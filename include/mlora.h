@@ -4,8 +4,9 @@
  * THE OPERATION
  *   A LoRA-adapted projection computes y = x·W + s·(x·A)·B with a per-adapter A (d_in x r),
  *   B (r x d_out) and scale s = alpha / r ("Multi-LoRA Serving, in depth", section "The
- *   computation, unmerged"). The shared base product x·W is NOT part of this library: the
- *   caller passes its result as y, and the library adds the low-rank delta in place.
+ *   computation, unmerged"). The adapters' calls do not compute the shared base product x·W: the
+ *   caller passes its result as y (lora_fp8_matmul makes it from 8-bit weights), and the
+ *   library adds the low-rank delta in place.
  *   Punica (arXiv 2310.18547), section 3.4 "The SGMV Operator", splits the delta into
  *       shrink   v = x·A        (d_in -> r; v starts from zero)
  *       expand   y += v·B       (r -> d_out, in place)
@@ -111,7 +112,7 @@ extern "C" {
 #define MLORA_STATUS_BAD_TOKEN 128    /* lora_logits_adjust: a token id outside the vocabulary */
 #define MLORA_STATUS_BAD_REQUEST 256  /* a row's request outside [0, num_requests) */
 
-typedef enum { MLORA_BF16 = 0, MLORA_FP16 = 1, MLORA_FP32 = 2 /* lora_logits_adjust only */ } mlora_dtype;
+typedef enum { MLORA_BF16 = 0, MLORA_FP16 = 1, MLORA_FP32 = 2 /* logits only */ } mlora_dtype;
 typedef enum { MLORA_POOL_STACKED = 0, MLORA_POOL_PAGED = 1 } mlora_pool_kind;
 
 /* One adapter pool for one projection shape (d_in -> d_out), every layer, every slot.
@@ -476,6 +477,107 @@ typedef struct {
 } mlora_logits;
 
 MLORA_API int lora_logits_adjust(const mlora_logits *args, int32_t *dev_status, void *stream);
+
+/* ---- the step around the adapters: norm, 8-bit rows, base product, next token ---------------
+ * What stands between the adapted projections of a step whose base weights are held in 8 bits: the norm with the
+ * residual's addition, the base products x W that the adapters add to, and the choice of the next token. The
+ * adapters read x in 16 bits, the base product reads it in 8, so the calls that make x write both.
+ *
+ * 8-bit rows: e4m3 values (1 sign, 4 exponent, 3 mantissa bits, largest 448) q [num_rows][ldq] with an fp32 scale for
+ * every block of MLORA_FP8_BLOCK columns of a row (the last may be shorter), scale [num_rows][lds]; an element
+ * stands for q * scale. Those of values v are
+ *   scale = max(max |v| of the block / 448, 2^-126),   q = v / scale rounded to the nearest e4m3, ties to even;
+ * a NaN makes its block's scale and values NaN, an infinity makes the scale an infinity, its own value NaN and the
+ * others 0. The conventions above hold: pointers of 16-bit and 8-bit arrays 16-byte aligned, their widths and
+ * leading dimensions multiples of 8 unless said, fp32 and int32 arrays 4-byte aligned. */
+
+#define MLORA_FP8_BLOCK 128
+#define MLORA_ROW_MAX_WIDTH 32768     /* lora_rms_norm */
+#define MLORA_SAMPLE_MAX_VOCAB 393216
+
+/* lora_rms_norm: with h = x + residual (x without one),
+ *   residual_out = round(h),   v = weight * h / sqrt(mean of h^2 over the row + eps),   out = round(v),
+ *   (q, q_scale) = v as 8-bit rows,
+ * in fp32 from the unrounded h, each output rounded once. residual and residual_out come together, and q and q_scale; out
+ * or q may be NULL, not both. residual_out may be residual or x, and out may be x or residual, with equal leading dimensions; no two
+ * outputs are the same array. Squares that pass fp32's range are summed scaled: a finite row has finite results. */
+typedef struct {
+  int32_t num_rows, width, dtype; /* width a multiple of 8, 8 .. MLORA_ROW_MAX_WIDTH; dtype of x, residual, weight, out */
+  float eps;                      /* > 0, finite */
+  const void *x;                  /* [num_rows][ldx] */
+  const void *residual;           /* [num_rows][ldr], or NULL */
+  const void *weight;             /* [width], or NULL: 1 */
+  void *residual_out;             /* [num_rows][ldro] */
+  void *out;                      /* [num_rows][ldo], or NULL */
+  void *q;                        /* [num_rows][ldq], or NULL */
+  float *q_scale;                 /* [num_rows][lds >= ceil(width / 128)] */
+  int64_t ldx, ldr, ldro, ldo, ldq, lds;
+} mlora_norm;
+
+MLORA_API int lora_rms_norm(const mlora_norm *args, void *stream);
+
+/* lora_quantize: v = x, or x * gate / (1 + exp(-gate)) with a gate, in fp32;
+ *   (q, q_scale) = v as 8-bit rows,   out = round(v)
+ * q (with q_scale) or out may be NULL, not both. out may be x or gate, with equal leading dimensions. gate and x may be column blocks
+ * of one array. 1 / (1 + exp(-gate)) is held to 2^-149. */
+typedef struct {
+  int32_t num_rows, width, dtype; /* width a multiple of 8, at least 8; dtype of x, gate, out */
+  const void *x;                  /* [num_rows][ldx] */
+  const void *gate;               /* [num_rows][ldg], or NULL */
+  void *out;                      /* [num_rows][ldo], or NULL */
+  void *q;                        /* [num_rows][ldq], or NULL */
+  float *q_scale;                 /* [num_rows][lds >= ceil(width / 128)] */
+  int64_t ldx, ldg, ldo, ldq, lds;
+} mlora_quant;
+
+MLORA_API int lora_quantize(const mlora_quant *args, void *stream);
+
+/* lora_fp8_matmul: y[i][n] = round( sum over blocks b of 128 columns of
+ *     x_scale[i][b] * w_scale[n / 128][b] * sum over k in b of x[i][k] w[n][k] ),
+ * the base product that lora_sgmv and lora_bgmv then add to. x: 8-bit rows; w: e4m3 [d_out][ldw >= d_in], the layout
+ * (out_features, in_features), with a scale for every block of 128 x 128. A block's products are summed by the tensor
+ * cores in fp32, the blocks in fp32 in a fixed order: the same call gives the same bits. y is no other array.
+ * TIMEOUT as for the adapters' calls. */
+typedef struct {
+  int32_t num_rows, d_in, d_out, dtype; /* d_in a multiple of 16, d_out of 8; dtype of y */
+  const void *x;                        /* [num_rows][ldx], ldx a multiple of 16 */
+  const float *x_scale;                 /* [num_rows][ldxs >= ceil(d_in / 128)] */
+  const void *w;                        /* [d_out][ldw], ldw a multiple of 16 */
+  const float *w_scale;                 /* [ceil(d_out / 128)][ldws >= ceil(d_in / 128)] */
+  void *y;                              /* [num_rows][ldy] */
+  int64_t ldx, ldxs, ldw, ldws, ldy;
+} mlora_matmul;
+
+MLORA_API int lora_fp8_matmul(const mlora_matmul *args, int32_t *dev_status, void *stream);
+
+/* lora_sample: the next token of row i, of request r = row_request[i] (-1: the row's outputs are left untouched), from a
+ * uniform random number in [0, 1). The tokens in the order of their logits, the largest first, equal ones by their
+ * id; with T = temperature[r], w_t = exp((logit_t - the largest logit) / T). A prefix of the order is kept, the shortest of
+ *   top_k[r] > 0:     the first top_k[r] tokens
+ *   top_p[r] < 1:     the fewest whose w sum to at least top_p[r] times the sum over those that top_k leaves
+ *   min_p[r] > 0:     the tokens with w_t >= min_p[r]
+ * and at least one token; token[i] is the first of the order at which the running sum of w exceeds uniform[i] times the sum
+ * over those kept, logprob[i] = log(its w / that sum). T <= 0: the first token of the order. Every array of the requests may be NULL and
+ * then has no part (T = 1). Behind lora_logits_adjust, the temperature is given to one of the two calls.
+ * A NaN logit counts as -inf; -inf has w = 0; of logits of +inf each has w = 1 and all others 0. A row with nothing but
+ * -inf gets token -1 and logprob -inf. uniform outside [0, 1) is taken to the nearer end, NaN as 0.
+ * The sums are of whole numbers, 2^-44 of the largest w each (w to 2^-36 of itself): the same bits on every call.
+ * Status: row_request[i] outside [-1, num_requests) (BAD_REQUEST): the row is skipped. */
+typedef struct {
+  int32_t num_rows, vocab, dtype; /* 1 <= vocab <= MLORA_SAMPLE_MAX_VOCAB; dtype: MLORA_FP32, MLORA_BF16 or MLORA_FP16 */
+  int32_t num_requests;
+  const void *logits;             /* [num_rows][ld >= vocab], aligned to their element */
+  int64_t ld;
+  const int32_t *row_request;     /* [num_rows], or NULL: row i is request i */
+  const float *uniform;           /* [num_rows] */
+  const float *temperature;       /* [num_requests] each, or NULL */
+  const int32_t *top_k;
+  const float *top_p, *min_p;
+  int32_t *token;                 /* [num_rows] */
+  float *logprob;                 /* [num_rows], or NULL */
+} mlora_sampling;
+
+MLORA_API int lora_sample(const mlora_sampling *args, int32_t *dev_status, void *stream);
 
 /* ---- utilities --------------------------------------------------------------------------- */
 

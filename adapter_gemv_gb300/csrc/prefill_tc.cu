@@ -25,11 +25,11 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
-#include <mutex>
 
 #include "common.cuh"
 #include "launch.h"
 #include "tc.cuh"
+#include "tensormap.h"
 
 namespace mlora {
 
@@ -761,23 +761,6 @@ __global__ void __launch_bounds__(EXP_THREADS, 2) tc_expand_kernel(const __grid_
 
 // ------------------------------------------------------------------------------------------
 // host
-
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encoder() {
-  static EncodeFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeFn>(p);
-  });
-  return fn;
-}
 
 // 2-D map over `rows` rows of `cols` 16-bit elements with a row pitch of `ld` elements;
 // box = 64 columns x box_rows rows, 128-byte swizzle, zero fill outside the tensor.

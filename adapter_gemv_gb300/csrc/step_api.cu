@@ -91,6 +91,7 @@ int lora_fp8_matmul(const mlora_matmul *a, int32_t *dev_status, void *stream) {
   if (!a) return MLORA_ERR_NULL;
   TRY(check_type(a->dtype));
   if (a->num_rows < 0 || a->d_in < 16 || a->d_out < 8) return MLORA_ERR_SHAPE;
+  if (a->d_out > INT32_MAX - 256) return MLORA_ERR_SHAPE;  // a tile's last column is counted in 31 bits
   if (a->d_in % 16 || a->d_out % 8) return MLORA_ERR_ALIGN;
   if (a->num_rows == 0) return MLORA_OK;
   const int64_t blocks = blocks_of(a->d_in);

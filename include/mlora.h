@@ -539,7 +539,7 @@ MLORA_API int lora_quantize(const mlora_quant *args, void *stream);
  * cores in fp32, the blocks in fp32 in a fixed order: the same call gives the same bits. y is no other array.
  * TIMEOUT as for the adapters' calls. */
 typedef struct {
-  int32_t num_rows, d_in, d_out, dtype; /* d_in a multiple of 16, d_out of 8; dtype of y */
+  int32_t num_rows, d_in, d_out, dtype; /* d_in a multiple of 16, d_out of 8 and below 2^31 - 256 */
   const void *x;                        /* [num_rows][ldx], ldx a multiple of 16 */
   const float *x_scale;                 /* [num_rows][ldxs >= ceil(d_in / 128)] */
   const void *w;                        /* [d_out][ldw], ldw a multiple of 16 */

@@ -63,7 +63,7 @@ def test_quantize_refusals(L, kw, code):  # noqa: F811
 
 @pytest.mark.parametrize("kw, code", [
     (dict(dtype=2), m.ERR_DTYPE), (dict(num_rows=-1), m.ERR_SHAPE), (dict(d_in=0), m.ERR_SHAPE), (dict(d_out=0), m.ERR_SHAPE),
-    (dict(d_in=264), m.ERR_ALIGN), (dict(d_out=132), m.ERR_ALIGN), (dict(x=0), m.ERR_NULL), (dict(w=0), m.ERR_NULL), (dict(y=0), m.ERR_NULL),
+    (dict(d_out=2 ** 31 - 128, ldy=2 ** 31), m.ERR_SHAPE), (dict(d_in=264), m.ERR_ALIGN), (dict(d_out=132), m.ERR_ALIGN), (dict(x=0), m.ERR_NULL), (dict(w=0), m.ERR_NULL), (dict(y=0), m.ERR_NULL),
     (dict(x_scale=0), m.ERR_NULL), (dict(w_scale=0), m.ERR_NULL), (dict(x=F + 8), m.ERR_ALIGN), (dict(w=G + 4), m.ERR_ALIGN),
     (dict(y=H + 8), m.ERR_ALIGN), (dict(x_scale=F + 2), m.ERR_ALIGN), (dict(ldx=256), m.ERR_SHAPE), (dict(ldx=280), m.ERR_ALIGN),
     (dict(ldw=280), m.ERR_ALIGN), (dict(ldw=256), m.ERR_SHAPE), (dict(ldxs=2), m.ERR_SHAPE), (dict(ldws=2), m.ERR_SHAPE),

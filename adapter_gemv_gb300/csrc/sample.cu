@@ -1,7 +1,18 @@
 // sample.cu -- the next token of each row from a given random number, with temperature, top-k, top-p and min-p (sm_103a).
 //
-// First form: a CTA a row; each limit is a place in the row's order (logits descending, then ids), found by bisection of
-// the order's code with a pass over the row for each of its bits.
+// Every limit, and the token itself, is a place in the row's order (logits descending, then ids): the k-th, or the first at
+// which the weights' running sum reaches a number. A place is found without sorting the row: a histogram of counts and weights
+// over the logarithm of the weight says in which bin it lies, and only that bin's tokens (with those before it where they are
+// few: they serve the next limits, too) are gathered, sorted and summed. Weights and sums are whole numbers
+// (sample_weight.cuh), so that the atomics' order does not matter.
+//
+// A cluster of 1 to 8 CTAs takes a row, each a stretch of its vocabulary, which it reads once and holds as fp32 in shared
+// memory. The first CTA does the searching; the others count, reduce and gather for it: it writes a command into
+// its shared memory, and all meet at the cluster's barrier before and behind its execution.
+//
+// Few tokens have a weight above 2^-12 of the largest, so that only those go to the histogram, with two atomics each; the
+// others are summed in registers and are one last bin. A bin of more than kList tokens, that one or one of many near or
+// equal logits, is divided again by the logits' bits, as often as it takes; equal logits are counted by their ids.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -15,120 +26,548 @@ namespace mlora {
 namespace {
 
 constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 512;           // and one more for what is smaller
+constexpr float kBinsPerLog2 = kBins / 12.f;
+constexpr int kList = 1024;
+constexpr int kMaxCtas = 8;
 constexpr int kIdBits = 19;
 static_assert(MLORA_SAMPLE_MAX_VOCAB <= 1 << kIdBits, "ids fit the order's code");
+static_assert(kBins == kThreads, "a thread a bin");
 
-template <int DT>
-__device__ __forceinline__ float logit_at(const mlora_sampling &p, int64_t row, int t) {
-  float x;
-  if constexpr (DT == MLORA_FP32) x = static_cast<const float *>(p.logits)[row * p.ld + t];
-  else x = Elem<DT>::lo(static_cast<const uint16_t *>(p.logits)[row * p.ld + t]);
-  return x == x ? x + 0.f : -CUDART_INF_F;  // (-0 as 0)
+enum Op { DONE, GATHER, RANGE, DIVIDE, TIES, TIE };
+struct Command {
+  int32_t op;
+  int32_t by_key;   // tokens of the bins lo .. hi, or of the keys lo .. hi
+  uint32_t lo, hi;
+  int32_t shift;    // DIVIDE: keys of a bin, as a power of two, from hi down
+  int32_t cta, nth; // TIE
+};
+
+struct Bins {  // counts and weights, or their running sums
+  uint32_t count[kBins + 1];
+  uint64_t mass[kBins + 1];
+};
+
+struct Smem {
+  Command cmd;
+  WeightScale scale;
+  float least;           // min_p as a logit
+  float top[kMaxCtas];   // (slot 0: this CTA's)
+  uint32_t low, high;    // of RANGE; count of TIES
+  int32_t found;         // TIE's token; the first token of the largest logit
+  int32_t listed;
+  uint64_t part[kWarps], sum;
+  uint32_t cpart[kWarps], csum;
+  float2 steps[kExp2Steps];
+  Bins bins;             // this CTA's; the first CTA's become the row's
+  Bins first, deep;      // the row's running sums: of the first division, of the last of a bin
+  uint64_t code[kList], cum[kList];
+};
+
+// Key: larger for larger logits. A place in the order is ~key, then the id.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float logit_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); }
+__device__ __forceinline__ uint64_t code_of(float x, int t) { return (uint64_t)~key_of(x) << kIdBits | (uint32_t)t; }
+
+// The bin of a logit: it does not fall as the logit falls. -1: weight 0.
+__device__ __forceinline__ int bin_of(float x, float top, float scale) {
+  const float y = (x - top) * scale;  // NaN for infinities of one sign
+  if (x == top) return 0;
+  if (!(y > -(float)(kWeightBits + 2))) return -1;
+  return (int)fminf(-y * kBinsPerLog2, (float)kBins);
 }
 
-// Place in the order: the larger logit first, then the lower id.
-__device__ __forceinline__ uint64_t code_of(float x, int t) {
-  const uint32_t b = __float_as_uint(x), up = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return (uint64_t)~up << kIdBits | (uint32_t)t;
-}
-
-__device__ __forceinline__ uint64_t sum_all(uint64_t v, uint64_t *part) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-  __syncthreads();
-  if (lane == 0) part[warp] = v;
-  __syncthreads();
-  v = lane < kThreads / 32 ? part[lane] : 0;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+__device__ __forceinline__ uint32_t dsmem_ld_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ uint64_t dsmem_ld_u64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void dsmem_st_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void dsmem_st_u64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t dsmem_add(uint32_t addr, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
+  return old;
+}
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ mlora_sampling p, int32_t *status) {
-  __shared__ float2 steps[kExp2Steps];
-  __shared__ uint64_t part[32];
-  __shared__ float tops[32];
+struct Vec {  // 16 bytes of logits
+  static constexpr int N = 8;
+  using T = uint16_t;
+  static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[N]) { unpack8<DT>(u, f); }
+  static __device__ __forceinline__ float get(T w) { return Elem<DT>::lo(w); }
+};
+template <>
+struct Vec<MLORA_FP32> {
+  static constexpr int N = 4;
+  using T = float;
+  static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[N]) {
+    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ float get(T w) { return w; }
+};
+
+__device__ __forceinline__ float cleaned(float x) { return x == x ? x + 0.f : -CUDART_INF_F; }  // NaN as -inf, -0 as 0
+
+// What a CTA of the cluster knows of its row.
+struct Row {
+  Smem &sh;
+  const float *x;   // this CTA's logits, in shared memory
+  int t0, n;        // its first token, how many
+  int cta, ctas;
+  float top;
+  WeightScale scale;
+
+  __device__ __forceinline__ void meet() const {
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+  }
+  __device__ __forceinline__ uint32_t of(const void *p, int c) const { return dsmem_addr(p, c); }
+
+  __device__ __forceinline__ bool in(const Command &c, float v) const {
+    const uint32_t at = c.by_key ? key_of(v) : (uint32_t)bin_of(v, top, scale.hi);
+    return at - c.lo <= c.hi - c.lo;  // (bin -1 is above every hi)
+  }
+
+  // Counts and weights of the cluster's CTAs, bin by bin, into the first CTA's bins; and there their running sums.
+  __device__ void reduce_bins(Bins &sums) {
+    meet();
+    if (ctas > 1) {
+      uint32_t count = 0;
+      uint64_t mass = 0;
+      // CTA c takes bins c, c + ctas, ..: at most one a thread, and the last bin
+      const int b0 = threadIdx.x * ctas + cta;
+      const bool mine = b0 <= kBins;
+      if (mine)
+        for (int c = 0; c < ctas; ++c) {
+          count += dsmem_ld_u32(of(&sh.bins.count[b0], c));
+          mass += dsmem_ld_u64(of(&sh.bins.mass[b0], c));
+        }
+      meet();
+      if (mine) {
+        dsmem_st_u32(of(&sh.bins.count[b0], 0), count);
+        dsmem_st_u64(of(&sh.bins.mass[b0], 0), mass);
+      }
+      meet();
+    }
+    if (cta == 0) {
+      const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+      uint32_t count = sh.bins.count[tid];
+      uint64_t mass = sh.bins.mass[tid];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t c = __shfl_up_sync(~0u, count, d);
+        const uint64_t m = __shfl_up_sync(~0u, mass, d);
+        if (lane >= d) count += c, mass += m;
+      }
+      if (lane == 31) sh.cpart[warp] = count, sh.part[warp] = mass;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) count += sh.cpart[w], mass += sh.part[w];
+      sums.count[tid] = count, sums.mass[tid] = mass;
+      if (tid == kThreads - 1) sums.count[kBins] = count + sh.bins.count[kBins], sums.mass[kBins] = mass + sh.bins.mass[kBins];
+      __syncthreads();
+    }
+  }
+
+  // Every CTA of the cluster executes the first one's command.
+  __device__ void execute(const Command &c) {
+    const int tid = threadIdx.x;
+    if (c.op == GATHER) {
+      const uint32_t counter = of(&sh.listed, 0);
+      for (int i = tid; i < n; i += kThreads) {
+        const float v = x[i];
+        if (!in(c, v)) continue;
+        const uint32_t at = dsmem_add(counter, 1);
+        if (at < (uint32_t)kList) dsmem_st_u64(of(&sh.code[at], 0), code_of(v, t0 + i));
+      }
+    } else if (c.op == RANGE) {
+      uint32_t low = ~0u, high = 0;
+      for (int i = tid; i < n; i += kThreads) {
+        const float v = x[i];
+        if (in(c, v)) low = min(low, key_of(v)), high = max(high, key_of(v));
+      }
+      if (tid == 0) sh.low = ~0u, sh.high = 0;
+      __syncthreads();
+      low = __reduce_min_sync(~0u, low), high = __reduce_max_sync(~0u, high);
+      if ((tid & 31) == 0) atomicMin(&sh.low, low), atomicMax(&sh.high, high);
+    } else if (c.op == DIVIDE) {
+      for (int i = tid; i <= kBins; i += kThreads) sh.bins.count[i] = 0, sh.bins.mass[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < n; i += kThreads) {
+        const float v = x[i];
+        if (!in(c, v)) continue;
+        const uint32_t b = (c.hi - key_of(v)) >> c.shift;
+        atomicAdd(&sh.bins.count[b], 1u);
+        atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[b]), (unsigned long long)weight_of(v, top, scale, sh.steps));
+      }
+      reduce_bins(sh.deep);
+    } else if (c.op == TIES) {
+      uint32_t ties = 0;
+      for (int i = tid; i < n; i += kThreads) ties += in(c, x[i]);
+      if (tid == 0) sh.low = 0;
+      __syncthreads();
+      ties = __reduce_add_sync(~0u, ties);
+      if ((tid & 31) == 0) atomicAdd(&sh.low, ties);
+    } else if (c.op == TIE && c.cta == cta) {
+      // the nth of this CTA's: thread by thread in stretches, so that the order is the ids'
+      const int each = (n + kThreads - 1) / kThreads, i0 = min(tid * each, n), i1 = min(i0 + each, n);
+      uint32_t ties = 0;
+      for (int i = i0; i < i1; ++i) ties += in(c, x[i]);
+      uint32_t before = ties;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(~0u, before, d);
+        if ((tid & 31) >= d) before += o;
+      }
+      if ((tid & 31) == 31) sh.cpart[tid >> 5] = before;
+      __syncthreads();
+      before -= ties;
+      for (int w = 0; w < tid >> 5; ++w) before += sh.cpart[w];
+      if ((uint32_t)c.nth >= before && (uint32_t)c.nth < before + ties)
+        for (int i = i0; i < i1; ++i)
+          if (in(c, x[i]) && before++ == (uint32_t)c.nth) dsmem_st_u32(of(&sh.found, 0), (uint32_t)(t0 + i));
+    }
+  }
+
+  // ---- the first CTA ------------------------------------------------------------------------------------
+  __device__ void command(Command c) {
+    if (threadIdx.x == 0) sh.cmd = c;
+    meet();
+    execute(c);
+    meet();
+  }
+
+  // Gathers, sorts and sums tokens of which there are at most kList, with `mass` before them.
+  __device__ void list(const Command &c, uint64_t mass) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) sh.listed = 0;
+    command(c);
+    const int m = min(sh.listed, kList);
+    if (m <= kThreads) {  // a token's place is the number of those before it
+      const uint64_t own = tid < m ? sh.code[tid] : 0;
+      int place = 0;
+#pragma unroll 4
+      for (int i = 0; i < m; ++i) place += sh.code[i] < own;
+      __syncthreads();
+      if (tid < m) sh.code[place] = own;
+    } else {  // bitonic, padded
+      for (int i = m + tid; i < kList; i += kThreads) sh.code[i] = ~0ull;
+      __syncthreads();
+      for (int size = 2; size <= kList; size <<= 1)
+        for (int step = size >> 1; step; step >>= 1) {
+          const int i = (tid / step) * 2 * step + tid % step, j = i + step;
+          const uint64_t a = sh.code[i], b = sh.code[j];
+          if ((a > b) == ((i & size) == 0)) sh.code[i] = b, sh.code[j] = a;
+          __syncthreads();
+        }
+    }
+    __syncthreads();
+    uint64_t w[kList / kThreads], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kList / kThreads; ++k) {
+      const int i = tid * (kList / kThreads) + k;
+      w[k] = i < m ? weight_of(logit_of(~(uint32_t)(sh.code[i] >> kIdBits)), top, scale, sh.steps) : 0;
+      sum += w[k];
+    }
+    uint64_t incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint64_t o = __shfl_up_sync(~0u, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) sh.part[warp] = incl;
+    __syncthreads();
+    mass += incl - sum;
+    for (int v = 0; v < warp; ++v) mass += sh.part[v];
+#pragma unroll
+    for (int k = 0; k < kList / kThreads; ++k) {
+      const int i = tid * (kList / kThreads) + k;
+      mass += w[k];
+      if (i < m) sh.cum[i] = mass;
+    }
+    __syncthreads();
+  }
+
+  // How many of the first `m` pass: all of them pass up to a place and none behind it.
+  template <class F>
+  __device__ int first_that_fails(int m, F passes) const {
+    int p = 0;
+    for (int i0 = 0; i0 < m; i0 += kThreads) p += __syncthreads_count(i0 + threadIdx.x < m && passes(i0 + threadIdx.x));
+    return p;
+  }
+
+  struct Place {
+    uint64_t mass;  // of the order up to and with it
+    int token;
+  };
+  enum Kind { COUNT, MASS, KEY };
+  int list_lo = 1, list_hi = 0;  // bins of the first division that the list holds
+
+  // COUNT: the place of the arg-th token; MASS: the first at which the running sum reaches arg; KEY: the sum over the logits with
+  // a key of at least arg (no token). There is such a place: arg is within the row's sums.
+  __device__ Place find(Kind kind, uint64_t arg) {
+    const Bins &s = sh.first;
+    const int b = kind == KEY ? bin_of(logit_of((uint32_t)arg), top, scale.hi)
+                              : first_that_fails(kBins, [&](int i) { return kind == COUNT ? s.count[i] < arg : s.mass[i] < arg; });
+    uint32_t count = b ? s.count[b - 1] : 0;
+    uint64_t mass = b ? s.mass[b - 1] : 0;
+    if (b < list_lo || b > list_hi) {
+      if (s.count[b] <= (uint32_t)kList) {
+        list(Command{GATHER, 0, 0, (uint32_t)b}, 0);
+        list_lo = 0, list_hi = b;
+      } else if (s.count[b] - count <= (uint32_t)kList) {
+        list(Command{GATHER, 0, (uint32_t)b, (uint32_t)b}, mass);
+        list_lo = list_hi = b;
+      } else {
+        return find_deep(kind, arg, Command{RANGE, 0, (uint32_t)b, (uint32_t)b}, count, mass);
+      }
+    }
+    return in_list(kind, arg, list_lo ? s.count[list_lo - 1] : 0, list_lo ? s.mass[list_lo - 1] : 0);
+  }
+
+  __device__ Place in_list(Kind kind, uint64_t arg, uint32_t count, uint64_t mass) {
+    const int m = min(sh.listed, kList);
+    const int p = kind == COUNT ? (int)(arg - 1 - count)
+                                : first_that_fails(m, [&](int i) {
+                                    return kind == MASS ? sh.cum[i] < arg : ~(uint32_t)(sh.code[i] >> kIdBits) >= (uint32_t)arg;
+                                  });
+    if (kind == KEY) return Place{p ? sh.cum[p - 1] : mass, -1};
+    return Place{sh.cum[p], (int)(sh.code[p] & ((1u << kIdBits) - 1))};
+  }
+
+  // The same in a bin of more than kList tokens, with `count` and `mass` before it.
+  __device__ Place find_deep(Kind kind, uint64_t arg, Command c, uint32_t count, uint64_t mass) {
+    list_lo = 1, list_hi = 0;
+    command(c);
+    uint32_t low = ~0u, high = 0;
+    for (int i = 0; i < ctas; ++i) low = min(low, dsmem_ld_u32(of(&sh.low, i))), high = max(high, dsmem_ld_u32(of(&sh.high, i)));
+    for (;;) {
+      if (low == high) return find_tie(kind, arg, low, count, mass);
+      int shift = 0;
+      while ((high - low) >> shift >= (uint32_t)kBins) ++shift;
+      command(Command{DIVIDE, 1, low, high, shift});
+      const Bins &s = sh.deep;
+      const int b = kind == KEY ? (uint32_t)arg > high ? 0 : (int)((high - max((uint32_t)arg, low)) >> shift)
+                                : first_that_fails(kBins - 1, [&](int i) { return kind == COUNT ? count + s.count[i] < arg : mass + s.mass[i] < arg; });
+      const uint32_t inside = s.count[b] - (b ? s.count[b - 1] : 0);
+      if (b) count += s.count[b - 1], mass += s.mass[b - 1];
+      const uint32_t top_key = high - ((uint32_t)b << shift);
+      low = max(low, top_key - ((1u << shift) - 1u)), high = top_key;
+      if (inside <= (uint32_t)kList) {
+        __syncthreads();
+        list(Command{GATHER, 1, low, high}, mass);
+        return in_list(kind, arg, count, mass);
+      }
+      __syncthreads();
+    }
+  }
+
+  // The same among more than kList equal logits: the first of their ids.
+  __device__ Place find_tie(Kind kind, uint64_t arg, uint32_t key, uint32_t count, uint64_t mass) {
+    const uint64_t w = weight_of(logit_of(key), top, scale, sh.steps);
+    Command c{TIES, 1, key, key};
+    command(c);
+    uint32_t ties = 0;
+    for (int i = 0; i < ctas; ++i) ties += dsmem_ld_u32(of(&sh.low, i));
+    if (kind == KEY) return Place{mass + ((uint32_t)arg <= key ? ties * w : 0), -1};
+    // (w is not 0 where a sum is reached among them)
+    uint64_t nth = kind == COUNT ? arg - 1 - count : w ? (arg - mass - 1) / w : 0;
+    const uint64_t up_to = mass + (nth + 1) * w;
+    int at = 0;
+    for (; at < ctas - 1; ++at) {
+      const uint32_t here = dsmem_ld_u32(of(&sh.low, at));
+      if (nth < here) break;
+      nth -= here;
+    }
+    c.op = TIE, c.cta = at, c.nth = (int)nth;
+    __syncthreads();
+    command(c);
+    return Place{up_to, sh.found};
+  }
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ mlora_sampling p, int32_t row0, int32_t ctas,
+                                                             int32_t stretch, int32_t *status) {
+  using V = Vec<DT>;
+  using T = typename V::T;
+  extern __shared__ __align__(16) uint8_t raw[];
+  Smem &sh = *reinterpret_cast<Smem *>(raw);
+  float *held = reinterpret_cast<float *>(raw + (sizeof(Smem) + 15) / 16 * 16);
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = row0 + blockIdx.x / ctas;
+  const int cta = blockIdx.x % ctas;
   const int r = p.row_request ? p.row_request[row] : (int)row;
-  if (r == -1) return;
-  if (r < -1 || r >= p.num_requests) {
-    if (tid == 0) report(status, MLORA_STATUS_BAD_REQUEST);
+  if (r < 0 || r >= p.num_requests) {  // (all CTAs of the cluster)
+    if (r != -1 && cta == 0 && tid == 0) report(status, MLORA_STATUS_BAD_REQUEST);
     return;
   }
-  for (int i = tid; i < kExp2Steps; i += kThreads) steps[i] = exp2_steps[i];
+  if (ctas > 1) cluster_arrive_relaxed();  // waited for before the first access to another CTA's shared memory
+  // ---- the stretch, as fp32, where 16-byte vectors of it are aligned in memory --------------------------------
+  const int t0 = cta * stretch, n = max(0, min(stretch, p.vocab - t0));
+  const T *src = static_cast<const T *>(p.logits) + row * p.ld + t0;
+  const int skew = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
+  float *x = held + skew;
   float top = -CUDART_INF_F;
-  for (int t = tid; t < p.vocab; t += kThreads) top = fmaxf(top, logit_at<DT>(p, row, t));
+#pragma unroll 4
+  for (int v = tid; v * V::N < n + skew; v += kThreads) {
+    const int t = v * V::N - skew;
+    float f[V::N];
+    if (t >= 0 && t + V::N <= n) {
+      V::unpack(ldg_u4(src + t), f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) f[e] = t + e >= 0 && t + e < n ? V::get(src[t + e]) : -CUDART_INF_F;
+    }
+#pragma unroll
+    for (int e = 0; e < V::N; ++e) f[e] = cleaned(f[e]), top = fmaxf(top, f[e]);
+#pragma unroll
+    for (int e = 0; e < V::N; e += 4) *reinterpret_cast<float4 *>(x + t + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+  }
+  // ---- the row's parameters, while the stretch is on its way ----------------------------------------------------
+  const float temp = p.temperature ? p.temperature[r] : 1.f;
+  int k = p.top_k ? p.top_k[r] : 0;
+  if (!(temp > 0.f)) k = 1;
+  const float limit = p.top_p ? p.top_p[r] : 1.f, least_p = p.min_p ? p.min_p[r] : 0.f;
+  if (tid == 0) sh.scale = weight_scale(temp > 0.f ? temp : 1.f);  // (in fp64, of which an SM does few)
+  for (int i = tid; i < kExp2Steps; i += kThreads) sh.steps[i] = exp2_steps[i];
+  for (int i = tid; i <= kBins; i += kThreads) sh.bins.count[i] = 0, sh.bins.mass[i] = 0;
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-  if ((tid & 31) == 0) tops[tid >> 5] = top;
+  if (lane == 0) sh.part[warp] = __float_as_uint(top);
   __syncthreads();
-  for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, tops[i]);
-  if (top == -CUDART_INF_F) {
-    if (tid == 0) {
-      p.token[row] = -1;
-      if (p.logprob) p.logprob[row] = -CUDART_INF_F;
-    }
-    return;
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, __uint_as_float((uint32_t)sh.part[w]));
+  if (ctas > 1) {
+    cluster_wait();
+    if (tid < ctas) dsmem_st_u32(dsmem_addr(&sh.top[cta], tid), __float_as_uint(top));
+    cluster_sync();
+    for (int c = 0; c < ctas; ++c) top = fmaxf(top, sh.top[c]);
   }
-  const float temp = p.temperature ? p.temperature[r] : 1.f;
-  const bool greedy = !(temp > 0.f);
-  const WeightScale scale = weight_scale(greedy ? 1.f : temp);
-  int k = p.top_k ? p.top_k[r] : 0;
-  if (greedy) k = 1;
-  if (k <= 0 || k > p.vocab) k = p.vocab;
-
-  auto sum = [&](uint64_t last, bool mass) {  // over the order up to the code `last`
-    uint64_t s = 0;
-    for (int t = tid; t < p.vocab; t += kThreads) {
-      const float x = logit_at<DT>(p, row, t);
-      if (code_of(x, t) <= last) s += mass ? weight_of(x, top, scale, steps) : 1;
+  Row me{sh, x, t0, n, cta, ctas, top, sh.scale};
+  int token = -1;
+  float logprob = -CUDART_INF_F;
+  if (top != -CUDART_INF_F && k == 1) {
+    // ---- the first token of the order ------------------------------------------------------------------------------
+    int first = INT32_MAX;
+    for (int i = tid; i < n; i += kThreads)
+      if (x[i] == top) first = min(first, t0 + i);
+    if (tid == 0) sh.found = INT32_MAX;
+    __syncthreads();
+    first = __reduce_min_sync(~0u, first);
+    if (lane == 0 && first != INT32_MAX) atomicMin(&sh.found, first);
+    me.meet();
+    token = INT32_MAX, logprob = 0.f;
+    if (cta == 0)
+      for (int c = 0; c < ctas; ++c) token = min(token, (int)dsmem_ld_u32(dsmem_addr(&sh.found, c)));
+    if (ctas > 1) cluster_sync();
+  } else if (top != -CUDART_INF_F) {
+    // ---- counts and weights by bins ------------------------------------------------------------------------------
+    {
+      uint32_t count = 0;
+      uint64_t mass = 0;
+      for (int i = tid; i < n; i += kThreads) {
+        const float v = x[i];
+        const int b = bin_of(v, top, me.scale.hi);
+        if (b < 0) continue;
+        const uint64_t w = weight_of(v, top, me.scale, sh.steps);
+        if (b == kBins) {
+          ++count, mass += w;
+        } else {
+          atomicAdd(&sh.bins.count[b], 1u);
+          atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[b]), (unsigned long long)w);
+        }
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) count += __shfl_xor_sync(~0u, count, d), mass += __shfl_xor_sync(~0u, mass, d);
+      if (lane == 0 && count) {
+        atomicAdd(&sh.bins.count[kBins], count);
+        atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[kBins]), (unsigned long long)mass);
+      }
+      me.reduce_bins(sh.first);
     }
-    return sum_all(s, part);
-  };
-  auto place = [&](uint64_t least, bool mass) {  // the first code at which the sum reaches `least`
-    uint64_t code = 0;
-    for (int b = 31 + kIdBits; b >= 0; --b)
-      if (sum(code | ((1ull << b) - 1), mass) < least) code |= 1ull << b;
-    return code;
-  };
-  uint64_t kept = sum(k < p.vocab ? place(k, false) : ~0ull, true);
-  const float tp = p.top_p ? p.top_p[r] : 1.f;
-  if (tp < 1.f) kept = sum(place(max(times_ceil(fmaxf(tp, 0.f), kept), (uint64_t)1), true), true);
-  const float mp = p.min_p ? p.min_p[r] : 0.f;
-  if (mp > 0.f) {
-    const float least = __double2float_ru((double)top + (double)temp * log((double)mp));
-    uint64_t s = 0;
-    for (int t = tid; t < p.vocab; t += kThreads) {
-      const float x = logit_at<DT>(p, row, t);
-      if (x >= least) s += weight_of(x, top, scale, steps);
+    if (cta == 0) {
+      // ---- the limits, each a shorter prefix of the order, and the token ------------------------------------
+      if (tid == 0 && least_p > 0.f && least_p < 1.f) sh.least = __double2float_ru((double)top + (double)temp * log((double)least_p));
+      uint64_t kept = sh.first.mass[kBins];
+      if (k > 0 && (uint32_t)k < sh.first.count[kBins]) kept = me.find(Row::COUNT, (uint64_t)k).mass;
+      if (limit < 1.f) {
+        const uint64_t goal = times_ceil(fmaxf(limit, 0.f), kept);
+        kept = me.find(Row::MASS, goal > 0 ? goal : 1).mass;
+      }
+      if (least_p > 0.f) {
+        __syncthreads();
+        const float least = least_p < 1.f ? sh.least : top;
+        uint64_t above = kWeightOne;  // at least the first token
+        if (least_p <= 1.f) above = bin_of(least, top, me.scale.hi) < 0 ? kept : max(me.find(Row::KEY, key_of(least + 0.f)).mass, kWeightOne);
+        kept = min(kept, above);
+      }
+      const float u = p.uniform[row];
+      const uint64_t goal = times_floor(u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f, kept) + 1;
+      token = me.find(Row::MASS, goal).token;
+      if (tid == 0) {
+        float y = 0.f, yl = 0.f;
+        const float chosen = cleaned(V::get(static_cast<const T *>(p.logits)[row * p.ld + token]));
+        if (chosen != top) weight_log2(chosen, top, me.scale, y, yl);
+        logprob = (y + yl) * 0.693147182f - log1pf((float)(kept - kWeightOne) * (1.f / (float)kWeightOne));
+        sh.cmd.op = DONE;
+      }
+      me.meet();
+    } else {
+      for (;;) {
+        me.meet();
+        Command c;
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(Command) / 4); ++i)
+          reinterpret_cast<uint32_t *>(&c)[i] = dsmem_ld_u32(dsmem_addr(reinterpret_cast<uint32_t *>(&sh.cmd) + i, 0));
+        if (c.op == DONE) break;
+        me.execute(c);
+        me.meet();
+      }
     }
-    kept = min(kept, max(sum_all(s, part), kWeightOne));
+    if (ctas > 1) cluster_sync();  // the last command has been read
   }
-  const float u = p.uniform[row];
-  const uint64_t code = place(times_floor(u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f, kept) + 1, true);
-  if (tid == 0) {
-    const int t = (int)(code & ((1u << kIdBits) - 1));
-    p.token[row] = t;
-    if (p.logprob) {
-      const float x = logit_at<DT>(p, row, t);
-      float y = 0.f, yl = 0.f;
-      if (x != top) weight_log2(x, top, scale, y, yl);
-      const float more = (float)(kept - kWeightOne) * (1.f / (float)kWeightOne);
-      p.logprob[row] = (y + yl) * 0.693147182f - log1pf(more);
-    }
+  if (cta == 0 && tid == 0) {
+    p.token[row] = token;
+    if (p.logprob) p.logprob[row] = logprob;
   }
 }
+
+constexpr size_t smem_bytes(int stretch) { return (sizeof(Smem) + 15) / 16 * 16 + (size_t)(stretch + 16) * sizeof(float); }
+constexpr int kMaxSmem = 227 * 1024;
+static_assert(smem_bytes(MLORA_SAMPLE_MAX_VOCAB / kMaxCtas) <= kMaxSmem, "a row fits in the shared memory of a cluster");
 
 template <int DT>
 cudaError_t launch(const mlora_sampling &p, int32_t *status, cudaStream_t stream) {
-  const cudaError_t e = launch_waiting(sample_kernel<DT>, dim3(p.num_rows), dim3(kThreads), 0, 1, stream, p, status);
-  if (e == cudaSuccess) api_count_launch();
-  return e;
+  // A stretch of at most 16384 tokens (64 KB, two CTAs an SM) where eight CTAs suffice for that; more CTAs for few rows.
+  int ctas = 1;
+  while (ctas < kMaxCtas && (p.vocab > 16384 * ctas || ((int64_t)p.num_rows * ctas * 2 <= sm_count() && p.vocab >= 2048 * ctas))) ctas *= 2;
+  const int stretch = ((p.vocab + ctas - 1) / ctas + 7) & ~7;
+  const size_t smem = smem_bytes(stretch);
+  cudaError_t e = raise_smem<sample_kernel<DT>>(kMaxSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t most = INT32_MAX / kMaxCtas;  // CTAs are counted in 31 bits
+  for (int64_t row0 = 0; row0 < p.num_rows; row0 += most) {
+    const dim3 grid((unsigned)(std::min<int64_t>(most, p.num_rows - row0) * ctas));
+    e = launch_waiting(sample_kernel<DT>, grid, dim3(kThreads), smem, ctas, stream, p, (int32_t)row0, ctas, stretch, status);
+    if (e != cudaSuccess) return e;
+    api_count_launch();
+  }
+  return cudaSuccess;
 }
 
 }  // namespace

@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "sample_weight.cuh"
+#include "tc.cuh"
 
 namespace mlora {
 
@@ -29,20 +30,23 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 512;           // and one more for what is smaller
 constexpr float kBinsPerLog2 = kBins / 12.f;
-constexpr int kList = 1024;
+constexpr int kList = kThreads;     // a thread a token
 constexpr int kMaxCtas = 8;
+constexpr int kRing = 8;
 constexpr int kIdBits = 19;
 static_assert(MLORA_SAMPLE_MAX_VOCAB <= 1 << kIdBits, "ids fit the order's code");
 static_assert(kBins == kThreads, "a thread a bin");
 
-enum Op { DONE, GATHER, RANGE, DIVIDE, TIES, TIE };
+enum Op { DONE, MASSES, GATHER, RANGE, DIVIDE, TIES, TIE };
 struct Command {
   int32_t op;
   int32_t by_key;   // tokens of the bins lo .. hi, or of the keys lo .. hi
   uint32_t lo, hi;
   int32_t shift;    // DIVIDE: keys of a bin, as a power of two, from hi down
   int32_t cta, nth; // TIE
+  float cut;        // no logit below is one of the tokens
 };
+constexpr int kCommandWords = sizeof(Command) / 4;
 
 struct Bins {  // counts and weights, or their running sums
   uint32_t count[kBins + 1];
@@ -50,15 +54,15 @@ struct Bins {  // counts and weights, or their running sums
 };
 
 struct Smem {
-  Command cmd;
-  WeightScale scale;
+  Command cmd;           // written by the first CTA
+  float top[kMaxCtas];
+  uint64_t sums[kMaxCtas];  // the weights of all tokens of the CTAs
   float least;           // min_p as a logit
-  float top[kMaxCtas];   // (slot 0: this CTA's)
   uint32_t low, high;    // of RANGE; count of TIES
   int32_t found;         // TIE's token; the first token of the largest logit
-  int32_t listed;
-  uint64_t part[kWarps], sum;
-  uint32_t cpart[kWarps], csum;
+  int32_t listed;        // tokens of the list; of this CTA's own before
+  uint64_t part[kWarps];
+  uint32_t cpart[kWarps];
   float2 steps[kExp2Steps];
   Bins bins;             // this CTA's; the first CTA's become the row's
   Bins first, deep;      // the row's running sums: of the first division, of the last of a bin
@@ -73,12 +77,16 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float logit_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); }
 __device__ __forceinline__ uint64_t code_of(float x, int t) { return (uint64_t)~key_of(x) << kIdBits | (uint32_t)t; }
 
-// The bin of a logit: it does not fall as the logit falls. -1: weight 0.
+// The bin of a logit: it does not fall as the logit falls. The last bin's tokens may have weight 0.
 __device__ __forceinline__ int bin_of(float x, float top, float scale) {
-  const float y = (x - top) * scale;  // NaN for infinities of one sign
-  if (x == top) return 0;
-  if (!(y > -(float)(kWeightBits + 2))) return -1;
-  return (int)fminf(-y * kBinsPerLog2, (float)kBins);
+  const float y = (top - x) * scale;  // (NaN for infinities of one sign)
+  return x == top ? 0 : y < (float)kBins ? (int)y : kBins;
+}
+// No logit below is in a bin up to b: by more than the roundings of bin_of.
+__device__ __forceinline__ float cut_of(int b, float top, float scale) {
+  if (b >= kBins) return -CUDART_INF_F;
+  const float by = (float)(b + 1) / scale;
+  return top - by - (by + fabsf(top)) * 0x1p-18f;  // (NaN, where nothing is cut, for an infinite top)
 }
 
 __device__ __forceinline__ uint32_t dsmem_ld_u32(uint32_t addr) {
@@ -123,82 +131,149 @@ struct Vec<MLORA_FP32> {
 __device__ __forceinline__ float cleaned(float x) { return x == x ? x + 0.f : -CUDART_INF_F; }  // NaN as -inf, -0 as 0
 
 // What a CTA of the cluster knows of its row.
+template <int DT>
 struct Row {
+  using V = Vec<DT>;
+  using T = typename V::T;
   Smem &sh;
-  const float *x;   // this CTA's logits, in shared memory
+  const T *src;     // this CTA's logits
+  const float *x;   // and in shared memory, where they are held
+  uint4 *ring;      // where not: what is on its way
   int t0, n;        // its first token, how many
   int cta, ctas;
   float top;
   WeightScale scale;
+  float bin_scale;
 
   __device__ __forceinline__ void meet() const {
     if (ctas > 1) cluster_sync();
     else __syncthreads();
   }
   __device__ __forceinline__ uint32_t of(const void *p, int c) const { return dsmem_addr(p, c); }
+  __device__ __forceinline__ float at(int i) const { return x ? x[i] : cleaned(V::get(src[i])); }
 
-  __device__ __forceinline__ bool in(const Command &c, float v) const {
-    const uint32_t at = c.by_key ? key_of(v) : (uint32_t)bin_of(v, top, scale.hi);
-    return at - c.lo <= c.hi - c.lo;  // (bin -1 is above every hi)
+  // f(logit, its place in this CTA's) for all of them, in no order. Where they are not held, each thread has kRing vectors of 16
+  // bytes on their way into places of its own in shared memory.
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    if (x) {
+#pragma unroll 2
+      for (int i = threadIdx.x; i < n; i += kThreads) f(x[i], i);
+      return;
+    }
+    const int skew = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
+    const T *from = src - skew;  // aligned
+    auto fetch = [&](int v, int slot) {
+      if (v * V::N >= skew && (v + 1) * V::N <= n + skew) tc::cp_async16(&ring[slot * kThreads + threadIdx.x], from + v * V::N, 16);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int j = 0; j < kRing; ++j) fetch(threadIdx.x + j * kThreads, j);
+    int slot = 0;
+#pragma unroll 1
+    for (int v = threadIdx.x; v * V::N < n + skew; v += kThreads) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      const int t = v * V::N - skew;
+      if (t >= 0 && t + V::N <= n) {
+        float w[V::N];
+        V::unpack(ring[slot * kThreads + threadIdx.x], w);
+        fetch(v + kRing * kThreads, slot);
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) f(cleaned(w[e]), t + e);
+      } else {
+        fetch(v + kRing * kThreads, slot);
+#pragma unroll 1
+        for (int e = max(-t, 0); e < V::N && t + e < n; ++e) f(cleaned(V::get(src[t + e])), t + e);
+      }
+      slot = (slot + 1) % kRing;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 
-  // Counts and weights of the cluster's CTAs, bin by bin, into the first CTA's bins; and there their running sums.
-  __device__ void reduce_bins(Bins &sums) {
+  __device__ __forceinline__ bool in(const Command &c, float v) const {
+    if (v < c.cut) return false;
+    const uint32_t at = c.by_key ? key_of(v) : (uint32_t)bin_of(v, top, bin_scale);
+    return at - c.lo <= c.hi - c.lo;
+  }
+  __device__ __forceinline__ uint64_t weight(float v) const { return weight_of(v, top, scale, sh.steps); }
+
+  // The running sums of the cluster's counts (and weights) over the bins, in the first CTA.
+  template <bool COUNTS, bool MASSES>
+  __device__ void sum_bins(Bins &sums) {
     meet();
-    if (ctas > 1) {
-      uint32_t count = 0;
-      uint64_t mass = 0;
-      // CTA c takes bins c, c + ctas, ..: at most one a thread, and the last bin
-      const int b0 = threadIdx.x * ctas + cta;
-      const bool mine = b0 <= kBins;
-      if (mine)
-        for (int c = 0; c < ctas; ++c) {
-          count += dsmem_ld_u32(of(&sh.bins.count[b0], c));
-          mass += dsmem_ld_u64(of(&sh.bins.mass[b0], c));
-        }
-      meet();
-      if (mine) {
-        dsmem_st_u32(of(&sh.bins.count[b0], 0), count);
-        dsmem_st_u64(of(&sh.bins.mass[b0], 0), mass);
-      }
-      meet();
-    }
-    if (cta == 0) {
-      const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-      uint32_t count = sh.bins.count[tid];
-      uint64_t mass = sh.bins.mass[tid];
+    if (cta != 0) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto row_of = [&](int b, uint32_t &count, uint64_t &mass) {
+      uint32_t k[kMaxCtas];
+      uint64_t m[kMaxCtas];
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t c = __shfl_up_sync(~0u, count, d);
-        const uint64_t m = __shfl_up_sync(~0u, mass, d);
-        if (lane >= d) count += c, mass += m;
+      for (int c = 0; c < kMaxCtas; ++c) {  // all on their way before the first is added
+        if (COUNTS) k[c] = c < ctas ? dsmem_ld_u32(of(&sh.bins.count[b], c)) : 0;
+        if (MASSES) m[c] = c < ctas ? dsmem_ld_u64(of(&sh.bins.mass[b], c)) : 0;
       }
-      if (lane == 31) sh.cpart[warp] = count, sh.part[warp] = mass;
-      __syncthreads();
-      for (int w = 0; w < warp; ++w) count += sh.cpart[w], mass += sh.part[w];
-      sums.count[tid] = count, sums.mass[tid] = mass;
-      if (tid == kThreads - 1) sums.count[kBins] = count + sh.bins.count[kBins], sums.mass[kBins] = mass + sh.bins.mass[kBins];
-      __syncthreads();
+      count = 0, mass = 0;
+#pragma unroll
+      for (int c = 0; c < kMaxCtas; ++c) {
+        if (COUNTS) count += k[c];
+        if (MASSES) mass += m[c];
+      }
+    };
+    uint32_t count, last_count = 0;
+    uint64_t mass, last_mass = 0;
+    row_of(tid, count, mass);
+    if (tid == kThreads - 1) row_of(kBins, last_count, last_mass);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t c = COUNTS ? __shfl_up_sync(~0u, count, d) : 0;
+      const uint64_t m = MASSES ? __shfl_up_sync(~0u, mass, d) : 0;
+      if (lane >= d) count += c, mass += m;
     }
+    if (lane == 31) sh.cpart[warp] = count, sh.part[warp] = mass;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) count += sh.cpart[w], mass += sh.part[w];
+    if (COUNTS) sums.count[tid] = count;
+    if (MASSES) sums.mass[tid] = mass;
+    if (tid == kThreads - 1) {
+      if (COUNTS) sums.count[kBins] = count + last_count;
+      if (MASSES) sums.mass[kBins] = mass + last_mass;
+    }
+    __syncthreads();
+  }
+
+  // Adds to the last bin's weight what the threads hold of it.
+  __device__ void add_last(uint64_t mass) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) mass += __shfl_xor_sync(~0u, mass, d);
+    if ((threadIdx.x & 31) == 0 && mass) atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[kBins]), (unsigned long long)mass);
   }
 
   // Every CTA of the cluster executes the first one's command.
   __device__ void execute(const Command &c) {
     const int tid = threadIdx.x;
-    if (c.op == GATHER) {
+    if (c.op == MASSES) {  // the weights of the first division's bins
+      for (int i = tid; i <= kBins; i += kThreads) sh.bins.mass[i] = 0;
+      __syncthreads();
+      uint64_t last = 0;
+      each([&](float v, int) {
+        const int b = bin_of(v, top, bin_scale);
+        const uint64_t w = weight(v);
+        if (b == kBins) last += w;
+        else atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[b]), (unsigned long long)w);
+      });
+      add_last(last);
+      sum_bins<false, true>(sh.first);
+    } else if (c.op == GATHER) {
       const uint32_t counter = of(&sh.listed, 0);
-      for (int i = tid; i < n; i += kThreads) {
-        const float v = x[i];
-        if (!in(c, v)) continue;
+      each([&](float v, int i) {
+        if (!in(c, v)) return;
         const uint32_t at = dsmem_add(counter, 1);
         if (at < (uint32_t)kList) dsmem_st_u64(of(&sh.code[at], 0), code_of(v, t0 + i));
-      }
+      });
     } else if (c.op == RANGE) {
       uint32_t low = ~0u, high = 0;
-      for (int i = tid; i < n; i += kThreads) {
-        const float v = x[i];
+      each([&](float v, int) {
         if (in(c, v)) low = min(low, key_of(v)), high = max(high, key_of(v));
-      }
+      });
       if (tid == 0) sh.low = ~0u, sh.high = 0;
       __syncthreads();
       low = __reduce_min_sync(~0u, low), high = __reduce_max_sync(~0u, high);
@@ -206,26 +281,25 @@ struct Row {
     } else if (c.op == DIVIDE) {
       for (int i = tid; i <= kBins; i += kThreads) sh.bins.count[i] = 0, sh.bins.mass[i] = 0;
       __syncthreads();
-      for (int i = tid; i < n; i += kThreads) {
-        const float v = x[i];
-        if (!in(c, v)) continue;
+      each([&](float v, int) {
+        if (!in(c, v)) return;
         const uint32_t b = (c.hi - key_of(v)) >> c.shift;
         atomicAdd(&sh.bins.count[b], 1u);
-        atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[b]), (unsigned long long)weight_of(v, top, scale, sh.steps));
-      }
-      reduce_bins(sh.deep);
+        atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[b]), (unsigned long long)weight(v));
+      });
+      sum_bins<true, true>(sh.deep);
     } else if (c.op == TIES) {
       uint32_t ties = 0;
-      for (int i = tid; i < n; i += kThreads) ties += in(c, x[i]);
+      each([&](float v, int) { ties += in(c, v); });
       if (tid == 0) sh.low = 0;
       __syncthreads();
       ties = __reduce_add_sync(~0u, ties);
       if ((tid & 31) == 0) atomicAdd(&sh.low, ties);
     } else if (c.op == TIE && c.cta == cta) {
       // the nth of this CTA's: thread by thread in stretches, so that the order is the ids'
-      const int each = (n + kThreads - 1) / kThreads, i0 = min(tid * each, n), i1 = min(i0 + each, n);
+      const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
       uint32_t ties = 0;
-      for (int i = i0; i < i1; ++i) ties += in(c, x[i]);
+      for (int i = i0; i < i1; ++i) ties += in(c, at(i));
       uint32_t before = ties;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -238,51 +312,54 @@ struct Row {
       for (int w = 0; w < tid >> 5; ++w) before += sh.cpart[w];
       if ((uint32_t)c.nth >= before && (uint32_t)c.nth < before + ties)
         for (int i = i0; i < i1; ++i)
-          if (in(c, x[i]) && before++ == (uint32_t)c.nth) dsmem_st_u32(of(&sh.found, 0), (uint32_t)(t0 + i));
+          if (in(c, at(i)) && before++ == (uint32_t)c.nth) dsmem_st_u32(of(&sh.found, 0), (uint32_t)(t0 + i));
     }
   }
 
   // ---- the first CTA ------------------------------------------------------------------------------------
-  __device__ void command(Command c) {
-    if (threadIdx.x == 0) sh.cmd = c;
+  __device__ void send(const Command &c) {
+    if (threadIdx.x < (unsigned)ctas) {
+      const uint32_t to = of(&sh.cmd, threadIdx.x);
+#pragma unroll
+      for (int i = 0; i < kCommandWords; ++i) dsmem_st_u32(to + i * 4, reinterpret_cast<const uint32_t *>(&c)[i]);
+    }
     meet();
+  }
+  __device__ void command(const Command &c) {
+    send(c);
     execute(c);
     meet();
   }
 
   // Gathers, sorts and sums tokens of which there are at most kList, with `mass` before them.
   __device__ void list(const Command &c, uint64_t mass) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) sh.listed = 0;
+    if (threadIdx.x == 0) sh.listed = 0;
     command(c);
-    const int m = min(sh.listed, kList);
-    if (m <= kThreads) {  // a token's place is the number of those before it
-      const uint64_t own = tid < m ? sh.code[tid] : 0;
-      int place = 0;
-#pragma unroll 4
-      for (int i = 0; i < m; ++i) place += sh.code[i] < own;
-      __syncthreads();
-      if (tid < m) sh.code[place] = own;
-    } else {  // bitonic, padded
-      for (int i = m + tid; i < kList; i += kThreads) sh.code[i] = ~0ull;
-      __syncthreads();
-      for (int size = 2; size <= kList; size <<= 1)
-        for (int step = size >> 1; step; step >>= 1) {
-          const int i = (tid / step) * 2 * step + tid % step, j = i + step;
-          const uint64_t a = sh.code[i], b = sh.code[j];
-          if ((a > b) == ((i & size) == 0)) sh.code[i] = b, sh.code[j] = a;
+    sort(min(sh.listed, kList), mass);
+  }
+  __device__ void sort(int m, uint64_t mass) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int size = 32;
+    while (size < m) size <<= 1;
+    // bitonic, a token a thread: between the lanes of a warp, and through shared memory where they are further apart
+    uint64_t own = tid < m ? sh.code[tid] : ~0ull;
+    for (int run = 2; run <= size; run <<= 1)
+      for (int step = run >> 1; step; step >>= 1) {
+        uint64_t other;
+        if (step < 32) {
+          other = __shfl_xor_sync(~0u, own, step);
+        } else {
           __syncthreads();
+          sh.code[tid] = own;
+          __syncthreads();
+          other = sh.code[tid ^ step];
         }
-    }
+        const bool smaller = ((tid & step) == 0) == ((tid & run) == 0);
+        if ((other < own) == smaller) own = other;
+      }
     __syncthreads();
-    uint64_t w[kList / kThreads], sum = 0;
-#pragma unroll
-    for (int k = 0; k < kList / kThreads; ++k) {
-      const int i = tid * (kList / kThreads) + k;
-      w[k] = i < m ? weight_of(logit_of(~(uint32_t)(sh.code[i] >> kIdBits)), top, scale, sh.steps) : 0;
-      sum += w[k];
-    }
-    uint64_t incl = sum;
+    const uint64_t w = tid < m ? weight(logit_of(~(uint32_t)(own >> kIdBits))) : 0;
+    uint64_t incl = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const uint64_t o = __shfl_up_sync(~0u, incl, d);
@@ -290,23 +367,16 @@ struct Row {
     }
     if (lane == 31) sh.part[warp] = incl;
     __syncthreads();
-    mass += incl - sum;
+    mass += incl;
     for (int v = 0; v < warp; ++v) mass += sh.part[v];
-#pragma unroll
-    for (int k = 0; k < kList / kThreads; ++k) {
-      const int i = tid * (kList / kThreads) + k;
-      mass += w[k];
-      if (i < m) sh.cum[i] = mass;
-    }
+    sh.code[tid] = own, sh.cum[tid] = mass;
     __syncthreads();
   }
 
   // How many of the first `m` pass: all of them pass up to a place and none behind it.
   template <class F>
   __device__ int first_that_fails(int m, F passes) const {
-    int p = 0;
-    for (int i0 = 0; i0 < m; i0 += kThreads) p += __syncthreads_count(i0 + threadIdx.x < m && passes(i0 + threadIdx.x));
-    return p;
+    return __syncthreads_count((int)threadIdx.x < m && passes((int)threadIdx.x));
   }
 
   struct Place {
@@ -315,27 +385,68 @@ struct Row {
   };
   enum Kind { COUNT, MASS, KEY };
   int list_lo = 1, list_hi = 0;  // bins of the first division that the list holds
+  bool masses = false;           // whether the bins' weights are there
+
+  __device__ Command bins_up_to(int b) const { return Command{GATHER, 0, 0, (uint32_t)b, 0, 0, 0, cut_of(b, top, bin_scale)}; }
+  // The first bins, as many as fit the list: of all but the last one the CTAs have kept the tokens as they counted them,
+  // where there are few; else up to bin `b`.
+  __device__ void list_first(int b) {
+    if (sh.first.count[kBins - 1] <= (uint32_t)kList) {
+      const int tid = threadIdx.x;
+      int before = 0, own = 0, from = 0;
+      for (int c = 0; c < ctas; ++c) {  // token tid of all
+        const int here = (int)dsmem_ld_u32(of(&sh.listed, c));
+        if (tid >= before && tid < before + here) own = tid - before, from = c;
+        before += here;
+      }
+      const uint64_t code = tid < before ? dsmem_ld_u64(of(&sh.code[own], from)) : 0;
+      __syncthreads();
+      sh.code[tid] = code;
+      if (tid == 0) sh.listed = before;
+      __syncthreads();
+      sort(before, 0);
+      list_lo = 0, list_hi = kBins - 1;
+      return;
+    }
+    const int fit = first_that_fails(kBins, [&](int i) { return sh.first.count[i] <= (uint32_t)kList; }) - 1;
+    if (fit < 0) return;
+    list(bins_up_to(min(b, fit)), 0);
+    list_lo = 0, list_hi = min(b, fit);
+  }
+  __device__ int bin_of_count(uint64_t k) const {
+    return first_that_fails(kBins, [&](int i) { return sh.first.count[i] < k; });
+  }
+  // Whether the list from the first token on answers by itself.
+  __device__ bool listed(Kind kind, uint64_t arg) const {
+    if (list_lo != 0 || list_hi < 0) return false;
+    if (kind == COUNT) return sh.first.count[list_hi] >= arg;
+    if (kind == KEY) return bin_of(logit_of((uint32_t)arg), top, bin_scale) <= list_hi;
+    const int m = min(sh.listed, kList);
+    return m > 0 && sh.cum[m - 1] >= arg;
+  }
 
   // COUNT: the place of the arg-th token; MASS: the first at which the running sum reaches arg; KEY: the sum over the logits with
   // a key of at least arg (no token). There is such a place: arg is within the row's sums.
   __device__ Place find(Kind kind, uint64_t arg) {
+    if (listed(kind, arg)) return in_list(kind, arg, 0, 0);
+    need_masses();
     const Bins &s = sh.first;
-    const int b = kind == KEY ? bin_of(logit_of((uint32_t)arg), top, scale.hi)
-                              : first_that_fails(kBins, [&](int i) { return kind == COUNT ? s.count[i] < arg : s.mass[i] < arg; });
-    uint32_t count = b ? s.count[b - 1] : 0;
-    uint64_t mass = b ? s.mass[b - 1] : 0;
+    const int b = kind == KEY ? bin_of(logit_of((uint32_t)arg), top, bin_scale)
+                              : kind == COUNT ? bin_of_count(arg) : first_that_fails(kBins, [&](int i) { return s.mass[i] < arg; });
+    const uint32_t count = b ? s.count[b - 1] : 0;
+    const uint64_t mass = b ? s.mass[b - 1] : 0;
     if (b < list_lo || b > list_hi) {
-      if (s.count[b] <= (uint32_t)kList) {
-        list(Command{GATHER, 0, 0, (uint32_t)b}, 0);
-        list_lo = 0, list_hi = b;
-      } else if (s.count[b] - count <= (uint32_t)kList) {
-        list(Command{GATHER, 0, (uint32_t)b, (uint32_t)b}, mass);
-        list_lo = list_hi = b;
-      } else {
-        return find_deep(kind, arg, Command{RANGE, 0, (uint32_t)b, (uint32_t)b}, count, mass);
-      }
+      if (s.count[b] - count > (uint32_t)kList) return find_deep(kind, arg, Command{RANGE, 0, (uint32_t)b, (uint32_t)b, 0, 0, 0, cut_of(b, top, bin_scale)}, count, mass);
+      Command c = bins_up_to(b);
+      c.lo = (uint32_t)b;
+      list(c, mass);
+      list_lo = list_hi = b;
     }
     return in_list(kind, arg, list_lo ? s.count[list_lo - 1] : 0, list_lo ? s.mass[list_lo - 1] : 0);
+  }
+  __device__ void need_masses() {
+    if (!masses) command(Command{MASSES});
+    masses = true;
   }
 
   __device__ Place in_list(Kind kind, uint64_t arg, uint32_t count, uint64_t mass) {
@@ -358,7 +469,7 @@ struct Row {
       if (low == high) return find_tie(kind, arg, low, count, mass);
       int shift = 0;
       while ((high - low) >> shift >= (uint32_t)kBins) ++shift;
-      command(Command{DIVIDE, 1, low, high, shift});
+      command(Command{DIVIDE, 1, low, high, shift, 0, 0, logit_of(low)});
       const Bins &s = sh.deep;
       const int b = kind == KEY ? (uint32_t)arg > high ? 0 : (int)((high - max((uint32_t)arg, low)) >> shift)
                                 : first_that_fails(kBins - 1, [&](int i) { return kind == COUNT ? count + s.count[i] < arg : mass + s.mass[i] < arg; });
@@ -368,7 +479,7 @@ struct Row {
       low = max(low, top_key - ((1u << shift) - 1u)), high = top_key;
       if (inside <= (uint32_t)kList) {
         __syncthreads();
-        list(Command{GATHER, 1, low, high}, mass);
+        list(Command{GATHER, 1, low, high, 0, 0, 0, logit_of(low)}, mass);
         return in_list(kind, arg, count, mass);
       }
       __syncthreads();
@@ -377,8 +488,8 @@ struct Row {
 
   // The same among more than kList equal logits: the first of their ids.
   __device__ Place find_tie(Kind kind, uint64_t arg, uint32_t key, uint32_t count, uint64_t mass) {
-    const uint64_t w = weight_of(logit_of(key), top, scale, sh.steps);
-    Command c{TIES, 1, key, key};
+    const uint64_t w = weight(logit_of(key));
+    Command c{TIES, 1, key, key, 0, 0, 0, logit_of(key)};
     command(c);
     uint32_t ties = 0;
     for (int i = 0; i < ctas; ++i) ties += dsmem_ld_u32(of(&sh.low, i));
@@ -401,7 +512,7 @@ struct Row {
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ mlora_sampling p, int32_t row0, int32_t ctas,
-                                                             int32_t stretch, int32_t *status) {
+                                                             int32_t stretch, bool hold, int32_t *status) {
   using V = Vec<DT>;
   using T = typename V::T;
   extern __shared__ __align__(16) uint8_t raw[];
@@ -418,54 +529,61 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return;
   }
   if (ctas > 1) cluster_arrive_relaxed();  // waited for before the first access to another CTA's shared memory
-  // ---- the stretch, as fp32, where 16-byte vectors of it are aligned in memory --------------------------------
+  // ---- the largest logit; the stretch into shared memory, as fp32, where 16-byte vectors of it are aligned ----------
   const int t0 = cta * stretch, n = max(0, min(stretch, p.vocab - t0));
   const T *src = static_cast<const T *>(p.logits) + row * p.ld + t0;
   const int skew = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
-  float *x = held + skew;
+  Row<DT> me{sh, src, nullptr, reinterpret_cast<uint4 *>(held), t0, n, cta, ctas};
   float top = -CUDART_INF_F;
+  if (hold) {
+    float *x = held + skew;
 #pragma unroll 4
-  for (int v = tid; v * V::N < n + skew; v += kThreads) {
-    const int t = v * V::N - skew;
-    float f[V::N];
-    if (t >= 0 && t + V::N <= n) {
-      V::unpack(ldg_u4(src + t), f);
-    } else {
+    for (int v = tid; v * V::N < n + skew; v += kThreads) {
+      const int t = v * V::N - skew;
+      float f[V::N];
+      if (t >= 0 && t + V::N <= n) {
+        V::unpack(ldg_u4(src + t), f);
+      } else {
 #pragma unroll
-      for (int e = 0; e < V::N; ++e) f[e] = t + e >= 0 && t + e < n ? V::get(src[t + e]) : -CUDART_INF_F;
+        for (int e = 0; e < V::N; ++e) f[e] = t + e >= 0 && t + e < n ? V::get(src[t + e]) : -CUDART_INF_F;
+      }
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) f[e] = cleaned(f[e]), top = fmaxf(top, f[e]);
+#pragma unroll
+      for (int e = 0; e < V::N; e += 4) *reinterpret_cast<float4 *>(x + t + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
     }
-#pragma unroll
-    for (int e = 0; e < V::N; ++e) f[e] = cleaned(f[e]), top = fmaxf(top, f[e]);
-#pragma unroll
-    for (int e = 0; e < V::N; e += 4) *reinterpret_cast<float4 *>(x + t + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+    me.x = x;
+  } else {
+    me.each([&](float v, int) { top = fmaxf(top, v); });
   }
-  // ---- the row's parameters, while the stretch is on its way ----------------------------------------------------
   const float temp = p.temperature ? p.temperature[r] : 1.f;
   int k = p.top_k ? p.top_k[r] : 0;
   if (!(temp > 0.f)) k = 1;
   const float limit = p.top_p ? p.top_p[r] : 1.f, least_p = p.min_p ? p.min_p[r] : 0.f;
-  if (tid == 0) sh.scale = weight_scale(temp > 0.f ? temp : 1.f);  // (in fp64, of which an SM does few)
   for (int i = tid; i < kExp2Steps; i += kThreads) sh.steps[i] = exp2_steps[i];
-  for (int i = tid; i <= kBins; i += kThreads) sh.bins.count[i] = 0, sh.bins.mass[i] = 0;
+  for (int i = tid; i <= kBins; i += kThreads) sh.bins.count[i] = 0;
+  if (tid == 0) sh.bins.mass[kBins] = 0;
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-  if (lane == 0) sh.part[warp] = __float_as_uint(top);
+  if (lane == 0) sh.cpart[warp] = __float_as_uint(top);
   __syncthreads();
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, __uint_as_float((uint32_t)sh.part[w]));
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, __uint_as_float(sh.cpart[w]));
   if (ctas > 1) {
     cluster_wait();
     if (tid < ctas) dsmem_st_u32(dsmem_addr(&sh.top[cta], tid), __float_as_uint(top));
     cluster_sync();
     for (int c = 0; c < ctas; ++c) top = fmaxf(top, sh.top[c]);
   }
-  Row me{sh, x, t0, n, cta, ctas, top, sh.scale};
+  me.top = top, me.scale = weight_scale(temp > 0.f ? temp : 1.f);
+  me.bin_scale = fminf(me.scale.hi * kBinsPerLog2, 3e38f);
   int token = -1;
   float logprob = -CUDART_INF_F;
   if (top != -CUDART_INF_F && k == 1) {
     // ---- the first token of the order ------------------------------------------------------------------------------
     int first = INT32_MAX;
-    for (int i = tid; i < n; i += kThreads)
-      if (x[i] == top) first = min(first, t0 + i);
+    me.each([&](float v, int i) {
+      if (v == top) first = min(first, t0 + i);
+    });
     if (tid == 0) sh.found = INT32_MAX;
     __syncthreads();
     first = __reduce_min_sync(~0u, first);
@@ -476,70 +594,80 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       for (int c = 0; c < ctas; ++c) token = min(token, (int)dsmem_ld_u32(dsmem_addr(&sh.found, c)));
     if (ctas > 1) cluster_sync();
   } else if (top != -CUDART_INF_F) {
-    // ---- counts and weights by bins ------------------------------------------------------------------------------
+    // ---- counts by bins; the sum of all weights, where it is asked for -----------------------------------------------------
+    const bool has_k = k > 0, has_p = limit < 1.f, has_min = least_p > 0.f;
+    const bool sum_all = !has_k && (has_p || !has_min);
+    if (cta == 0 && tid == kThreads - 1 && has_min && least_p < 1.f)
+      sh.least = __double2float_ru((double)top + (double)temp * log((double)least_p));
     {
-      uint32_t count = 0;
+      const float cut = cut_of(kBins - 1, top, me.bin_scale);
+      if (tid == 0) sh.listed = 0;
+      __syncthreads();
       uint64_t mass = 0;
-      for (int i = tid; i < n; i += kThreads) {
-        const float v = x[i];
-        const int b = bin_of(v, top, me.scale.hi);
-        if (b < 0) continue;
-        const uint64_t w = weight_of(v, top, me.scale, sh.steps);
-        if (b == kBins) {
-          ++count, mass += w;
-        } else {
-          atomicAdd(&sh.bins.count[b], 1u);
-          atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[b]), (unsigned long long)w);
+      me.each([&](float v, int i) {
+        if (sum_all) mass += me.weight(v);
+        if (v < cut) return;
+        const int b = bin_of(v, top, me.bin_scale);
+        if (b == kBins) return;
+        atomicAdd(&sh.bins.count[b], 1u);
+        if (*reinterpret_cast<volatile int32_t *>(&sh.listed) < kList) {
+          const int at = atomicAdd(&sh.listed, 1);
+          if (at < kList) sh.code[at] = code_of(v, t0 + i);
         }
+      });
+      if (sum_all) {
+        me.add_last(mass);  // (of all tokens)
+        __syncthreads();
+        if (tid == 0) dsmem_st_u64(me.of(&sh.sums[cta], 0), sh.bins.mass[kBins]);
       }
-#pragma unroll
-      for (int d = 16; d; d >>= 1) count += __shfl_xor_sync(~0u, count, d), mass += __shfl_xor_sync(~0u, mass, d);
-      if (lane == 0 && count) {
-        atomicAdd(&sh.bins.count[kBins], count);
-        atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[kBins]), (unsigned long long)mass);
-      }
-      me.reduce_bins(sh.first);
+      me.template sum_bins<true, false>(sh.first);
+      if (cta == 0 && tid == 0) sh.first.count[kBins] = (uint32_t)p.vocab;  // (the last bin is not counted)
+      if (cta == 0) __syncthreads();
     }
     if (cta == 0) {
       // ---- the limits, each a shorter prefix of the order, and the token ------------------------------------
-      if (tid == 0 && least_p > 0.f && least_p < 1.f) sh.least = __double2float_ru((double)top + (double)temp * log((double)least_p));
-      uint64_t kept = sh.first.mass[kBins];
-      if (k > 0 && (uint32_t)k < sh.first.count[kBins]) kept = me.find(Row::COUNT, (uint64_t)k).mass;
-      if (limit < 1.f) {
-        const uint64_t goal = times_ceil(fmaxf(limit, 0.f), kept);
-        kept = me.find(Row::MASS, goal > 0 ? goal : 1).mass;
+      const float least = least_p < 1.f ? sh.least : top;
+      const int least_bin = has_min && least_p <= 1.f ? bin_of(least, top, me.bin_scale) : kBins;
+      const bool all_k = !has_k || k >= p.vocab;
+      me.list_first(!all_k ? min(me.bin_of_count((uint64_t)k), kBins - 1) : has_min && !has_p ? min(least_bin, kBins - 1) : kBins - 1);
+      uint64_t kept = ~0ull;
+      if (sum_all) {
+        kept = 0;
+        for (int c = 0; c < ctas; ++c) kept += sh.sums[c];
+      } else if (!all_k) {
+        kept = me.find(Row<DT>::COUNT, (uint64_t)k).mass;
+      } else if (has_p || least_bin == kBins) {
+        me.need_masses();
+        kept = sh.first.mass[kBins];
       }
-      if (least_p > 0.f) {
-        __syncthreads();
-        const float least = least_p < 1.f ? sh.least : top;
+      if (has_p) {
+        const uint64_t goal = times_ceil(fmaxf(limit, 0.f), kept);
+        kept = me.find(Row<DT>::MASS, goal > 0 ? goal : 1).mass;
+      }
+      if (has_min) {
         uint64_t above = kWeightOne;  // at least the first token
-        if (least_p <= 1.f) above = bin_of(least, top, me.scale.hi) < 0 ? kept : max(me.find(Row::KEY, key_of(least + 0.f)).mass, kWeightOne);
+        if (least_p <= 1.f) above = max(me.find(Row<DT>::KEY, key_of(least + 0.f)).mass, kWeightOne);
         kept = min(kept, above);
       }
       const float u = p.uniform[row];
       const uint64_t goal = times_floor(u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f, kept) + 1;
-      token = me.find(Row::MASS, goal).token;
+      token = me.find(Row<DT>::MASS, goal).token;
       if (tid == 0) {
         float y = 0.f, yl = 0.f;
         const float chosen = cleaned(V::get(static_cast<const T *>(p.logits)[row * p.ld + token]));
         if (chosen != top) weight_log2(chosen, top, me.scale, y, yl);
         logprob = (y + yl) * 0.693147182f - log1pf((float)(kept - kWeightOne) * (1.f / (float)kWeightOne));
-        sh.cmd.op = DONE;
       }
-      me.meet();
+      if (ctas > 1) me.send(Command{DONE});
     } else {
       for (;;) {
         me.meet();
-        Command c;
-#pragma unroll
-        for (int i = 0; i < (int)(sizeof(Command) / 4); ++i)
-          reinterpret_cast<uint32_t *>(&c)[i] = dsmem_ld_u32(dsmem_addr(reinterpret_cast<uint32_t *>(&sh.cmd) + i, 0));
+        const Command c = sh.cmd;
         if (c.op == DONE) break;
         me.execute(c);
         me.meet();
       }
     }
-    if (ctas > 1) cluster_sync();  // the last command has been read
   }
   if (cta == 0 && tid == 0) {
     p.token[row] = token;
@@ -549,21 +677,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 constexpr size_t smem_bytes(int stretch) { return (sizeof(Smem) + 15) / 16 * 16 + (size_t)(stretch + 16) * sizeof(float); }
 constexpr int kMaxSmem = 227 * 1024;
-static_assert(smem_bytes(MLORA_SAMPLE_MAX_VOCAB / kMaxCtas) <= kMaxSmem, "a row fits in the shared memory of a cluster");
 
 template <int DT>
 cudaError_t launch(const mlora_sampling &p, int32_t *status, cudaStream_t stream) {
-  // A stretch of at most 16384 tokens (64 KB, two CTAs an SM) where eight CTAs suffice for that; more CTAs for few rows.
+  // Two CTAs an SM, as far as the rows leave it and the stretches stay long
   int ctas = 1;
-  while (ctas < kMaxCtas && (p.vocab > 16384 * ctas || ((int64_t)p.num_rows * ctas * 2 <= sm_count() && p.vocab >= 2048 * ctas))) ctas *= 2;
+  while (ctas < kMaxCtas && (int64_t)p.num_rows * ctas * 2 <= 2 * sm_count() && p.vocab >= 2048 * ctas) ctas *= 2;
   const int stretch = ((p.vocab + ctas - 1) / ctas + 7) & ~7;
-  const size_t smem = smem_bytes(stretch);
+  // held in shared memory where that does not cost CTAs their SM, read again (from L2, mostly) where it does
+  const bool hold = smem_bytes(stretch) <= (((int64_t)p.num_rows * ctas > sm_count()) ? kMaxSmem / 2 - 1024 : kMaxSmem);
+  const size_t smem = hold ? smem_bytes(stretch) : smem_bytes(0) + kRing * kThreads * 16;
   cudaError_t e = raise_smem<sample_kernel<DT>>(kMaxSmem);
   if (e != cudaSuccess) return e;
   const int64_t most = INT32_MAX / kMaxCtas;  // CTAs are counted in 31 bits
   for (int64_t row0 = 0; row0 < p.num_rows; row0 += most) {
     const dim3 grid((unsigned)(std::min<int64_t>(most, p.num_rows - row0) * ctas));
-    e = launch_waiting(sample_kernel<DT>, grid, dim3(kThreads), smem, ctas, stream, p, (int32_t)row0, ctas, stretch, status);
+    e = launch_waiting(sample_kernel<DT>, grid, dim3(kThreads), smem, ctas, stream, p, (int32_t)row0, ctas, stretch, hold, status);
     if (e != cudaSuccess) return e;
     api_count_launch();
   }

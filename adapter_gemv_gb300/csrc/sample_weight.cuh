@@ -5,7 +5,8 @@
 // by 2^-22 of themselves would put one number in a hundred on the wrong side. GB300 has few fp64 units, so the
 // exponential is worked out in pairs of fp32 (hi + lo): the exponent's product with its remainder, a table
 // of 2^(j/64) with its remainder, and 2^r for |r| <= 1/128 by the series of the exponential. The result is off by
-// 2^-36 of itself at most, found over 4 M random x, max and T, beside the rounding to 2^-44.
+// 2^-36 of itself at most, found over 4 M random x, max and T, beside the rounding to 2^-44; weights below 2^-18
+// are off by 2^-40 of the largest.
 #pragma once
 
 #include "serve.cuh"
@@ -43,10 +44,11 @@ struct WeightScale {
   float hi, lo;
 };
 __device__ __forceinline__ WeightScale weight_scale(float temperature) {
-  const double c = 1.4426950408889634074 / (double)temperature;
+  constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f;  // log2(e)
   WeightScale s;
-  s.hi = c < 3e38 ? (float)c : 3e38f;  // (beyond: every token below the largest has weight 0)
-  s.lo = c < 3e38 ? (float)(c - (double)s.hi) : 0.f;
+  s.hi = fminf(kHi / temperature, 3e38f);  // (there: every token below the largest has weight 0)
+  s.lo = s.hi < 3e38f ? (fmaf(-s.hi, temperature, kHi) + kLo) / temperature : 0.f;
+  if (!(fabsf(s.lo) < 3e38f)) s.lo = 0.f;  // (an infinite temperature: every weight is 1)
   return s;
 }
 
@@ -65,6 +67,12 @@ __device__ __forceinline__ uint64_t weight_of(float x, float top, const WeightSc
   if (x == top) y = yl = 0.f;
   if (!(y > -(float)(kWeightBits + 2))) return 0;  // (also -inf, and its product with 0)
   const float k = rintf(y), f = y - k;             // 2^k 2^f, |f| <= 1/2
+  // Below 2^-18 fp32's exponential is as exact: off by 2^-22 of itself, 2^-40 of the largest weight.
+  if (y < -18.f) {
+    float w;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(f + yl));
+    return (uint64_t)__float2uint_rn(w * __int_as_float(((int)k + kWeightBits + 127) << 23));
+  }
   const float j = rintf(f * 64.f), r = fmaf(j, -1.f / 64.f, f);
   // (r + yl) ln 2 = z + zl
   constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;

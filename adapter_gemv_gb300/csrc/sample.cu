@@ -29,7 +29,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 512;           // and one more for what is smaller
-constexpr float kBinsPerLog2 = kBins / 12.f;
+constexpr float kShort = 12.f, kLong = 24.f;  // log2 units that they cover, without the row's sum of weights and with it
 constexpr int kList = kThreads;     // a thread a token
 constexpr int kMaxCtas = 8;
 constexpr int kRing = 8;
@@ -37,14 +37,14 @@ constexpr int kIdBits = 19;
 static_assert(MLORA_SAMPLE_MAX_VOCAB <= 1 << kIdBits, "ids fit the order's code");
 static_assert(kBins == kThreads, "a thread a bin");
 
-enum Op { DONE, MASSES, GATHER, RANGE, DIVIDE, TIES, TIE };
+enum Op { DONE, MASSES, GATHER, DIVIDE, TIES, TIE };
 struct Command {
   int32_t op;
-  int32_t by_key;   // tokens of the bins lo .. hi, or of the keys lo .. hi
-  uint32_t lo, hi;
-  int32_t shift;    // DIVIDE: keys of a bin, as a power of two, from hi down
-  int32_t cta, nth; // TIE
-  float cut;        // no logit below is one of the tokens
+  float cut;          // the tokens of a logit of at least cut,
+  int32_t lo, hi;     // of the bins lo .. hi,
+  uint32_t low, high; // of the keys low .. high
+  int32_t shift;      // DIVIDE: keys of a bin, as a power of two, from high down
+  int32_t cta, nth;   // TIE
 };
 constexpr int kCommandWords = sizeof(Command) / 4;
 
@@ -56,9 +56,8 @@ struct Bins {  // counts and weights, or their running sums
 struct Smem {
   Command cmd;           // written by the first CTA
   float top[kMaxCtas];
-  uint64_t sums[kMaxCtas];  // the weights of all tokens of the CTAs
   float least;           // min_p as a logit
-  uint32_t low, high;    // of RANGE; count of TIES
+  uint32_t ties;         // count of TIES
   int32_t found;         // TIE's token; the first token of the largest logit
   int32_t listed;        // tokens of the list; of this CTA's own before
   uint64_t part[kWarps];
@@ -152,16 +151,24 @@ struct Row {
   __device__ __forceinline__ uint32_t of(const void *p, int c) const { return dsmem_addr(p, c); }
   __device__ __forceinline__ float at(int i) const { return x ? x[i] : cleaned(V::get(src[i])); }
 
-  // f(logit, its place in this CTA's) for all of them, in no order. Where they are not held, each thread has kRing vectors of 16
-  // bytes on their way into places of its own in shared memory.
+  // f(four logits, the first one's place in this CTA's) for all of them, in no order; a place before the first or behind the
+  // last has -inf. Whole warps. Where the logits are not held, each thread has kRing vectors of 16 bytes on their way into places of
+  // its own in shared memory.
   template <class F>
-  __device__ __forceinline__ void each(F f) const {
+  __device__ __forceinline__ void each4(F f) const {
+    const int skew = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
     if (x) {
-#pragma unroll 2
-      for (int i = threadIdx.x; i < n; i += kThreads) f(x[i], i);
+      const float4 *from = reinterpret_cast<const float4 *>(x - skew);
+      const int vectors = (n + skew + 3) / 4;
+#pragma unroll 1
+      for (int v0 = 0; v0 < vectors; v0 += kThreads) {
+        const int v = v0 + threadIdx.x;
+        const float4 u = v < vectors ? from[v] : make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+        const float w[4] = {u.x, u.y, u.z, u.w};
+        f(w, v * 4 - skew);
+      }
       return;
     }
-    const int skew = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
     const T *from = src - skew;  // aligned
     auto fetch = [&](int v, int slot) {
       if (v * V::N >= skew && (v + 1) * V::N <= n + skew) tc::cp_async16(&ring[slot * kThreads + threadIdx.x], from + v * V::N, 16);
@@ -171,31 +178,51 @@ struct Row {
     for (int j = 0; j < kRing; ++j) fetch(threadIdx.x + j * kThreads, j);
     int slot = 0;
 #pragma unroll 1
-    for (int v = threadIdx.x; v * V::N < n + skew; v += kThreads) {
+    for (int v0 = 0; v0 * V::N < n + skew; v0 += kThreads) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-      const int t = v * V::N - skew;
+      const int v = v0 + threadIdx.x, t = v * V::N - skew;
+      float w[V::N];
       if (t >= 0 && t + V::N <= n) {
-        float w[V::N];
         V::unpack(ring[slot * kThreads + threadIdx.x], w);
-        fetch(v + kRing * kThreads, slot);
-#pragma unroll
-        for (int e = 0; e < V::N; ++e) f(cleaned(w[e]), t + e);
       } else {
-        fetch(v + kRing * kThreads, slot);
-#pragma unroll 1
-        for (int e = max(-t, 0); e < V::N && t + e < n; ++e) f(cleaned(V::get(src[t + e])), t + e);
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) w[e] = t + e >= 0 && t + e < n ? V::get(src[t + e]) : -CUDART_INF_F;
       }
+      fetch(v + kRing * kThreads, slot);
       slot = (slot + 1) % kRing;
+#pragma unroll
+      for (int e = 0; e < V::N; e += 4) {
+        const float u[4] = {cleaned(w[e]), cleaned(w[e + 1]), cleaned(w[e + 2]), cleaned(w[e + 3])};
+        f(u, t + e);
+      }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  // The same, one by one.
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    each4([&](const float (&v)[4], int i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f(v[e], i + e);
+    });
   }
 
   __device__ __forceinline__ bool in(const Command &c, float v) const {
     if (v < c.cut) return false;
-    const uint32_t at = c.by_key ? key_of(v) : (uint32_t)bin_of(v, top, bin_scale);
-    return at - c.lo <= c.hi - c.lo;
+    const int b = bin_of(v, top, bin_scale);
+    return b >= c.lo && b <= c.hi && key_of(v) - c.low <= c.high - c.low;
   }
-  __device__ __forceinline__ uint64_t weight(float v) const { return weight_of(v, top, scale, sh.steps); }
+  __device__ __forceinline__ void weights(const float (&v)[4], uint64_t (&w)[4]) const { weights_of(v, top, scale, sh.steps, w); }
+  // (whole warps)
+  __device__ __forceinline__ uint64_t weight(float v) const {
+    const float x1[1] = {v};
+    uint64_t w[1];
+    weights_of(x1, top, scale, sh.steps, w);
+    return w[0];
+  }
+  __device__ __forceinline__ void add_mass(int b, uint64_t w) const {
+    atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[b]), (unsigned long long)w);
+  }
 
   // The running sums of the cluster's counts (and weights) over the bins, in the first CTA.
   template <bool COUNTS, bool MASSES>
@@ -240,11 +267,25 @@ struct Row {
     __syncthreads();
   }
 
-  // Adds to the last bin's weight what the threads hold of it.
-  __device__ void add_last(uint64_t mass) {
+  // Adds every token's weight to its bin's; those of the last bin are summed in registers first.
+  __device__ __forceinline__ void add_masses() {
+    uint64_t last = 0;
+    each4([&](const float (&v)[4], int) {
+      uint64_t w[4];
+      weights(v, w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int b = bin_of(v[e], top, bin_scale);
+        if (b == kBins) last += w[e];
+        else add_mass(b, w[e]);
+      }
+    });
+    add_last(last);
+  }
+  __device__ __forceinline__ void add_last(uint64_t mass) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) mass += __shfl_xor_sync(~0u, mass, d);
-    if ((threadIdx.x & 31) == 0 && mass) atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[kBins]), (unsigned long long)mass);
+    if ((threadIdx.x & 31) == 0 && mass) add_mass(kBins, mass);
   }
 
   // Every CTA of the cluster executes the first one's command.
@@ -253,48 +294,41 @@ struct Row {
     if (c.op == MASSES) {  // the weights of the first division's bins
       for (int i = tid; i <= kBins; i += kThreads) sh.bins.mass[i] = 0;
       __syncthreads();
-      uint64_t last = 0;
-      each([&](float v, int) {
-        const int b = bin_of(v, top, bin_scale);
-        const uint64_t w = weight(v);
-        if (b == kBins) last += w;
-        else atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[b]), (unsigned long long)w);
-      });
-      add_last(last);
+      add_masses();
       sum_bins<false, true>(sh.first);
     } else if (c.op == GATHER) {
       const uint32_t counter = of(&sh.listed, 0);
       each([&](float v, int i) {
-        if (!in(c, v)) return;
+        if (!in(c, v) || (uint32_t)i >= (uint32_t)n) return;
         const uint32_t at = dsmem_add(counter, 1);
         if (at < (uint32_t)kList) dsmem_st_u64(of(&sh.code[at], 0), code_of(v, t0 + i));
       });
-    } else if (c.op == RANGE) {
-      uint32_t low = ~0u, high = 0;
-      each([&](float v, int) {
-        if (in(c, v)) low = min(low, key_of(v)), high = max(high, key_of(v));
-      });
-      if (tid == 0) sh.low = ~0u, sh.high = 0;
-      __syncthreads();
-      low = __reduce_min_sync(~0u, low), high = __reduce_max_sync(~0u, high);
-      if ((tid & 31) == 0) atomicMin(&sh.low, low), atomicMax(&sh.high, high);
     } else if (c.op == DIVIDE) {
       for (int i = tid; i <= kBins; i += kThreads) sh.bins.count[i] = 0, sh.bins.mass[i] = 0;
       __syncthreads();
-      each([&](float v, int) {
-        if (!in(c, v)) return;
-        const uint32_t b = (c.hi - key_of(v)) >> c.shift;
-        atomicAdd(&sh.bins.count[b], 1u);
-        atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins.mass[b]), (unsigned long long)weight(v));
+      each4([&](const float (&v)[4], int) {
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any |= !(v[e] < c.cut);
+        if (!__any_sync(~0u, any)) return;
+        uint64_t w[4];
+        weights(v, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!in(c, v[e])) continue;
+          const uint32_t b = (c.high - key_of(v[e])) >> c.shift;
+          atomicAdd(&sh.bins.count[b], 1u);
+          add_mass(b, w[e]);
+        }
       });
       sum_bins<true, true>(sh.deep);
     } else if (c.op == TIES) {
       uint32_t ties = 0;
-      each([&](float v, int) { ties += in(c, v); });
-      if (tid == 0) sh.low = 0;
+      each([&](float v, int i) { ties += in(c, v) && (uint32_t)i < (uint32_t)n; });
+      if (tid == 0) sh.ties = 0;
       __syncthreads();
       ties = __reduce_add_sync(~0u, ties);
-      if ((tid & 31) == 0) atomicAdd(&sh.low, ties);
+      if ((tid & 31) == 0) atomicAdd(&sh.ties, ties);
     } else if (c.op == TIE && c.cta == cta) {
       // the nth of this CTA's: thread by thread in stretches, so that the order is the ids'
       const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
@@ -358,7 +392,8 @@ struct Row {
         if ((other < own) == smaller) own = other;
       }
     __syncthreads();
-    const uint64_t w = tid < m ? weight(logit_of(~(uint32_t)(own >> kIdBits))) : 0;
+    uint64_t w = weight(tid < m ? logit_of(~(uint32_t)(own >> kIdBits)) : top);
+    if (tid >= m) w = 0;
     uint64_t incl = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -387,7 +422,7 @@ struct Row {
   int list_lo = 1, list_hi = 0;  // bins of the first division that the list holds
   bool masses = false;           // whether the bins' weights are there
 
-  __device__ Command bins_up_to(int b) const { return Command{GATHER, 0, 0, (uint32_t)b, 0, 0, 0, cut_of(b, top, bin_scale)}; }
+  __device__ Command bins_of(int op, int lo, int hi) const { return Command{op, cut_of(hi, top, bin_scale), lo, hi, 0, ~0u, 0, 0, 0}; }
   // The first bins, as many as fit the list: of all but the last one the CTAs have kept the tokens as they counted them,
   // where there are few; else up to bin `b`.
   __device__ void list_first(int b) {
@@ -410,8 +445,13 @@ struct Row {
     }
     const int fit = first_that_fails(kBins, [&](int i) { return sh.first.count[i] <= (uint32_t)kList; }) - 1;
     if (fit < 0) return;
-    list(bins_up_to(min(b, fit)), 0);
+    list(bins_of(GATHER, 0, min(b, fit)), 0);
     list_lo = 0, list_hi = min(b, fit);
+  }
+  // No logit above is in a bin behind b.
+  __device__ float bin_end(int b) const {
+    const float by = (float)(b + 1) / bin_scale;
+    return top - by + (by + fabsf(top)) * 0x1p-18f;
   }
   __device__ int bin_of_count(uint64_t k) const {
     return first_that_fails(kBins, [&](int i) { return sh.first.count[i] < k; });
@@ -436,10 +476,8 @@ struct Row {
     const uint32_t count = b ? s.count[b - 1] : 0;
     const uint64_t mass = b ? s.mass[b - 1] : 0;
     if (b < list_lo || b > list_hi) {
-      if (s.count[b] - count > (uint32_t)kList) return find_deep(kind, arg, Command{RANGE, 0, (uint32_t)b, (uint32_t)b, 0, 0, 0, cut_of(b, top, bin_scale)}, count, mass);
-      Command c = bins_up_to(b);
-      c.lo = (uint32_t)b;
-      list(c, mass);
+      if (s.count[b] - count > (uint32_t)kList) return find_deep(kind, arg, b, count, mass);
+      list(bins_of(GATHER, b, b), mass);
       list_lo = list_hi = b;
     }
     return in_list(kind, arg, list_lo ? s.count[list_lo - 1] : 0, list_lo ? s.mass[list_lo - 1] : 0);
@@ -460,16 +498,21 @@ struct Row {
   }
 
   // The same in a bin of more than kList tokens, with `count` and `mass` before it.
-  __device__ Place find_deep(Kind kind, uint64_t arg, Command c, uint32_t count, uint64_t mass) {
+  __device__ Place find_deep(Kind kind, uint64_t arg, int bin, uint32_t count, uint64_t mass) {
     list_lo = 1, list_hi = 0;
-    command(c);
-    uint32_t low = ~0u, high = 0;
-    for (int i = 0; i < ctas; ++i) low = min(low, dsmem_ld_u32(of(&sh.low, i))), high = max(high, dsmem_ld_u32(of(&sh.high, i)));
+    Command c = bins_of(DIVIDE, bin, bin);
+    // keys that the bin's lie between
+    uint32_t low = key_of(c.cut == c.cut ? c.cut : -CUDART_INF_F), high = key_of(top);
+    if (bin > 0) {
+      const float before = bin_end(bin - 1);
+      if (before < top) high = key_of(before + 0.f);
+    }
     for (;;) {
       if (low == high) return find_tie(kind, arg, low, count, mass);
       int shift = 0;
       while ((high - low) >> shift >= (uint32_t)kBins) ++shift;
-      command(Command{DIVIDE, 1, low, high, shift, 0, 0, logit_of(low)});
+      c.op = DIVIDE, c.low = low, c.high = high, c.shift = shift;
+      command(c);
       const Bins &s = sh.deep;
       const int b = kind == KEY ? (uint32_t)arg > high ? 0 : (int)((high - max((uint32_t)arg, low)) >> shift)
                                 : first_that_fails(kBins - 1, [&](int i) { return kind == COUNT ? count + s.count[i] < arg : mass + s.mass[i] < arg; });
@@ -479,7 +522,8 @@ struct Row {
       low = max(low, top_key - ((1u << shift) - 1u)), high = top_key;
       if (inside <= (uint32_t)kList) {
         __syncthreads();
-        list(Command{GATHER, 1, low, high, 0, 0, 0, logit_of(low)}, mass);
+        c.op = GATHER, c.low = low, c.high = high, c.cut = logit_of(low);
+        list(c, mass);
         return in_list(kind, arg, count, mass);
       }
       __syncthreads();
@@ -489,17 +533,17 @@ struct Row {
   // The same among more than kList equal logits: the first of their ids.
   __device__ Place find_tie(Kind kind, uint64_t arg, uint32_t key, uint32_t count, uint64_t mass) {
     const uint64_t w = weight(logit_of(key));
-    Command c{TIES, 1, key, key, 0, 0, 0, logit_of(key)};
+    Command c{TIES, logit_of(key), 0, kBins, key, key, 0, 0, 0};
     command(c);
     uint32_t ties = 0;
-    for (int i = 0; i < ctas; ++i) ties += dsmem_ld_u32(of(&sh.low, i));
+    for (int i = 0; i < ctas; ++i) ties += dsmem_ld_u32(of(&sh.ties, i));
     if (kind == KEY) return Place{mass + ((uint32_t)arg <= key ? ties * w : 0), -1};
     // (w is not 0 where a sum is reached among them)
     uint64_t nth = kind == COUNT ? arg - 1 - count : w ? (arg - mass - 1) / w : 0;
     const uint64_t up_to = mass + (nth + 1) * w;
     int at = 0;
     for (; at < ctas - 1; ++at) {
-      const uint32_t here = dsmem_ld_u32(of(&sh.low, at));
+      const uint32_t here = dsmem_ld_u32(of(&sh.ties, at));
       if (nth < here) break;
       nth -= here;
     }
@@ -561,8 +605,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (!(temp > 0.f)) k = 1;
   const float limit = p.top_p ? p.top_p[r] : 1.f, least_p = p.min_p ? p.min_p[r] : 0.f;
   for (int i = tid; i < kExp2Steps; i += kThreads) sh.steps[i] = exp2_steps[i];
-  for (int i = tid; i <= kBins; i += kThreads) sh.bins.count[i] = 0;
-  if (tid == 0) sh.bins.mass[kBins] = 0;
+  for (int i = tid; i <= kBins; i += kThreads) sh.bins.count[i] = 0, sh.bins.mass[i] = 0;
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
   if (lane == 0) sh.cpart[warp] = __float_as_uint(top);
@@ -575,7 +618,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     for (int c = 0; c < ctas; ++c) top = fmaxf(top, sh.top[c]);
   }
   me.top = top, me.scale = weight_scale(temp > 0.f ? temp : 1.f);
-  me.bin_scale = fminf(me.scale.hi * kBinsPerLog2, 3e38f);
+  const bool sum_all = k <= 0 && (limit < 1.f || !(least_p > 0.f));  // whether the limits begin with the sum of all weights
+  me.bin_scale = fminf(me.scale.hi * (kBins / (sum_all ? kLong : kShort)), 3e38f);
   int token = -1;
   float logprob = -CUDART_INF_F;
   if (top != -CUDART_INF_F && k == 1) {
@@ -596,31 +640,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   } else if (top != -CUDART_INF_F) {
     // ---- counts by bins; the sum of all weights, where it is asked for -----------------------------------------------------
     const bool has_k = k > 0, has_p = limit < 1.f, has_min = least_p > 0.f;
-    const bool sum_all = !has_k && (has_p || !has_min);
     if (cta == 0 && tid == kThreads - 1 && has_min && least_p < 1.f)
       sh.least = __double2float_ru((double)top + (double)temp * log((double)least_p));
     {
       const float cut = cut_of(kBins - 1, top, me.bin_scale);
       if (tid == 0) sh.listed = 0;
       __syncthreads();
-      uint64_t mass = 0;
-      me.each([&](float v, int i) {
-        if (sum_all) mass += me.weight(v);
-        if (v < cut) return;
-        const int b = bin_of(v, top, me.bin_scale);
-        if (b == kBins) return;
-        atomicAdd(&sh.bins.count[b], 1u);
-        if (*reinterpret_cast<volatile int32_t *>(&sh.listed) < kList) {
-          const int at = atomicAdd(&sh.listed, 1);
-          if (at < kList) sh.code[at] = code_of(v, t0 + i);
+      uint64_t last = 0;
+      me.each4([&](const float (&v)[4], int i) {
+        uint64_t w[4];
+        if (sum_all) me.weights(v, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int b = v[e] < cut ? kBins : bin_of(v[e], top, me.bin_scale);
+          if (b < kBins) {
+            atomicAdd(&sh.bins.count[b], 1u);
+            if (sum_all) me.add_mass(b, w[e]);
+            if (*reinterpret_cast<volatile int32_t *>(&sh.listed) < kList) {
+              const int at = atomicAdd(&sh.listed, 1);
+              if (at < kList) sh.code[at] = code_of(v[e], t0 + i + e);
+            }
+          } else if (sum_all) {
+            last += w[e];
+          }
         }
       });
-      if (sum_all) {
-        me.add_last(mass);  // (of all tokens)
-        __syncthreads();
-        if (tid == 0) dsmem_st_u64(me.of(&sh.sums[cta], 0), sh.bins.mass[kBins]);
-      }
-      me.template sum_bins<true, false>(sh.first);
+      if (sum_all) me.add_last(last);
+      if (sum_all) me.template sum_bins<true, true>(sh.first);
+      else me.template sum_bins<true, false>(sh.first);
+      me.masses = sum_all;
       if (cta == 0 && tid == 0) sh.first.count[kBins] = (uint32_t)p.vocab;  // (the last bin is not counted)
       if (cta == 0) __syncthreads();
     }
@@ -632,8 +680,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       me.list_first(!all_k ? min(me.bin_of_count((uint64_t)k), kBins - 1) : has_min && !has_p ? min(least_bin, kBins - 1) : kBins - 1);
       uint64_t kept = ~0ull;
       if (sum_all) {
-        kept = 0;
-        for (int c = 0; c < ctas; ++c) kept += sh.sums[c];
+        kept = sh.first.mass[kBins];
       } else if (!all_k) {
         kept = me.find(Row<DT>::COUNT, (uint64_t)k).mass;
       } else if (has_p || least_bin == kBins) {

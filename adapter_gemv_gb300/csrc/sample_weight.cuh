@@ -9,6 +9,8 @@
 // are off by 2^-40 of the largest.
 #pragma once
 
+#include <math_constants.h>
+
 #include "serve.cuh"
 
 namespace mlora {
@@ -60,32 +62,51 @@ __device__ __forceinline__ void weight_log2(float x, float top, const WeightScal
   lo = fmaf(s, c.hi, -hi) + fmaf(s, c.lo, e * c.hi);
 }
 
-// The weight, 0 .. 2^44, of a logit that is no NaN; `steps`: exp2_steps in shared memory.
-__device__ __forceinline__ uint64_t weight_of(float x, float top, const WeightScale &c, const float2 *steps) {
-  float y, yl;
-  weight_log2(x, top, c, y, yl);
-  if (x == top) y = yl = 0.f;
-  if (!(y > -(float)(kWeightBits + 2))) return 0;  // (also -inf, and its product with 0)
-  const float k = rintf(y), f = y - k;             // 2^k 2^f, |f| <= 1/2
-  // Below 2^-18 fp32's exponential is as exact: off by 2^-22 of itself, 2^-40 of the largest weight.
-  if (y < -18.f) {
-    float w;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(f + yl));
-    return (uint64_t)__float2uint_rn(w * __int_as_float(((int)k + kWeightBits + 127) << 23));
+// The weights, 0 .. 2^44, of N logits that are no NaN; `steps`: exp2_steps in shared memory. Whole warps: what no lane needs is
+// left out (far below the largest logit, the weights that fp32 holds exactly enough), the rest is without branches.
+template <int N>
+__device__ __forceinline__ void weights_of(const float (&x)[N], float top, const WeightScale &c, const float2 *steps, uint64_t (&w)[N]) {
+  float y[N], yl[N], most = -CUDART_INF_F;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    weight_log2(x[i], top, c, y[i], yl[i]);
+    if (x[i] == top) y[i] = yl[i] = 0.f;
+    if (!(y[i] > -(float)(kWeightBits + 2))) y[i] = -(float)(kWeightBits + 2), yl[i] = 0.f;  // (also -inf, and its product with 0)
+    most = fmaxf(most, y[i]);
+    w[i] = 0;
   }
-  const float j = rintf(f * 64.f), r = fmaf(j, -1.f / 64.f, f);
-  // (r + yl) ln 2 = z + zl
-  constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;
-  const float z = r * kLn2Hi, zl = fmaf(r, kLn2Hi, -z) + fmaf(r, kLn2Lo, yl * kLn2Hi);
-  const float q = z * z * fmaf(z, fmaf(z, 1.f / 24.f, 1.f / 6.f), 0.5f);  // z^2/2 + z^3/6 + z^4/24; the next is 2^-44
-  const float2 t = steps[(int)j + 32];
-  // (t.x + t.y) (1 + z + zl + q + z zl) = h + l; zl^2 / 2 is below 2^-38
-  const float a = t.x * z, al = fmaf(t.x, z, -a);
-  const float h = t.x + a;
-  const float l = ((t.x - h) + a) + (al + fmaf(t.x, fmaf(z, zl, zl + q), fmaf(t.y, z, t.y)));
-  const int shift = -(int)k;
-  const int64_t whole = ((int64_t)__float2int_rn(h * 0x1p24f) << (kWeightBits - 24)) + (int64_t)__float2int_rn(l * 0x1p44f);
-  return (uint64_t)(shift ? (whole + (1ll << (shift - 1))) >> shift : whole);
+  if (!__any_sync(~0u, most > -(float)(kWeightBits + 2))) return;
+  if (!__any_sync(~0u, most >= -18.f)) {
+    // Below 2^-18 fp32's exponential is as exact: off by 2^-22 of itself, 2^-40 of the largest weight.
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float k = rintf(y[i]);
+      float f;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(y[i] - k + yl[i]));
+      w[i] = __float2uint_rn(f * __int_as_float(((int)k + kWeightBits + 127) << 23));
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float k = rintf(y[i]), f = y[i] - k;  // 2^k 2^f, |f| <= 1/2
+    const float j = rintf(f * 64.f), r = fmaf(j, -1.f / 64.f, f);
+    // (r + yl) ln 2 = z + zl
+    constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;
+    const float z = r * kLn2Hi, zl = fmaf(r, kLn2Hi, -z) + fmaf(r, kLn2Lo, yl[i] * kLn2Hi);
+    const float q = z * z * fmaf(z, fmaf(z, 1.f / 24.f, 1.f / 6.f), 0.5f);  // z^2/2 + z^3/6 + z^4/24; the next is 2^-44
+    const float2 t = steps[(int)j + 32];
+    // (t.x + t.y) (1 + z + zl + q + z zl) = h + l; zl^2 / 2 is below 2^-38
+    const float a = t.x * z, al = fmaf(t.x, z, -a);
+    const float h = t.x + a;
+    const float l = ((t.x - h) + a) + (al + fmaf(t.x, fmaf(z, zl, zl + q), fmaf(t.y, z, t.y)));
+    const int shift = -(int)k;
+    const uint64_t whole = (uint64_t)(((int64_t)__float2int_rn(h * 0x1p24f) << (kWeightBits - 24)) + (int64_t)__float2int_rn(l * 0x1p44f));
+    // (below 2^-18 a weight is the one above, whatever its neighbours are)
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f + yl[i]));
+    w[i] = y[i] < -18.f ? (uint64_t)__float2uint_rn(e * __int_as_float(((int)k + kWeightBits + 127) << 23)) : (whole + ((1ull << shift) >> 1)) >> shift;
+  }
 }
 
 // floor(f s) and ceil(f s) for 0 <= f < 1, exactly: f = m 2^-e with m below 2^24.

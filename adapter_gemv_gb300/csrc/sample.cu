@@ -29,7 +29,9 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 512;           // and one more for what is smaller
-constexpr float kShort = 12.f, kLong = 24.f;  // log2 units that they cover, without the row's sum of weights and with it
+// log2 units of the weights that they cover: with top_k, which may ask for tokens of any weight; with the sum of all weights; and
+// those whose tokens the CTAs keep as they count them
+constexpr float kRangeOfK = 46.f, kRangeOfSum = 24.f, kNear = 8.f;
 constexpr int kList = kThreads;     // a thread a token
 constexpr int kMaxCtas = 8;
 constexpr int kRing = 8;
@@ -267,21 +269,7 @@ struct Row {
     __syncthreads();
   }
 
-  // Adds every token's weight to its bin's; those of the last bin are summed in registers first.
-  __device__ __forceinline__ void add_masses() {
-    uint64_t last = 0;
-    each4([&](const float (&v)[4], int) {
-      uint64_t w[4];
-      weights(v, w);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int b = bin_of(v[e], top, bin_scale);
-        if (b == kBins) last += w[e];
-        else add_mass(b, w[e]);
-      }
-    });
-    add_last(last);
-  }
+  // Adds to the last bin's weight what the threads hold of it.
   __device__ __forceinline__ void add_last(uint64_t mass) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) mass += __shfl_xor_sync(~0u, mass, d);
@@ -291,10 +279,26 @@ struct Row {
   // Every CTA of the cluster executes the first one's command.
   __device__ void execute(const Command &c) {
     const int tid = threadIdx.x;
-    if (c.op == MASSES) {  // the weights of the first division's bins
+    if (c.op == MASSES) {  // the weights of the first division's bins 0 .. hi
       for (int i = tid; i <= kBins; i += kThreads) sh.bins.mass[i] = 0;
       __syncthreads();
-      add_masses();
+      uint64_t last = 0;
+      each4([&](const float (&v)[4], int) {
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any |= !(v[e] < c.cut);
+        if (!__any_sync(~0u, any)) return;
+        uint64_t w[4];
+        weights(v, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int b = bin_of(v[e], top, bin_scale);
+          if (b > c.hi) continue;
+          if (b == kBins) last += w[e];
+          else add_mass(b, w[e]);
+        }
+      });
+      add_last(last);
       sum_bins<false, true>(sh.first);
     } else if (c.op == GATHER) {
       const uint32_t counter = of(&sh.listed, 0);
@@ -420,13 +424,13 @@ struct Row {
   };
   enum Kind { COUNT, MASS, KEY };
   int list_lo = 1, list_hi = 0;  // bins of the first division that the list holds
-  bool masses = false;           // whether the bins' weights are there
+  int masses_hi = -1;            // up to which bin their weights are there
 
   __device__ Command bins_of(int op, int lo, int hi) const { return Command{op, cut_of(hi, top, bin_scale), lo, hi, 0, ~0u, 0, 0, 0}; }
-  // The first bins, as many as fit the list: of all but the last one the CTAs have kept the tokens as they counted them,
-  // where there are few; else up to bin `b`.
-  __device__ void list_first(int b) {
-    if (sh.first.count[kBins - 1] <= (uint32_t)kList) {
+  // The first bins up to bin `b`, or as many as fit the list. Those near the largest logit have been kept as they were counted, where
+  // they are few.
+  __device__ void list_first(int b, bool wanted, int near) {
+    if (sh.first.count[near - 1] <= (uint32_t)kList && (b < near || !wanted)) {
       const int tid = threadIdx.x;
       int before = 0, own = 0, from = 0;
       for (int c = 0; c < ctas; ++c) {  // token tid of all
@@ -440,11 +444,11 @@ struct Row {
       if (tid == 0) sh.listed = before;
       __syncthreads();
       sort(before, 0);
-      list_lo = 0, list_hi = kBins - 1;
+      list_lo = 0, list_hi = near - 1;
       return;
     }
     const int fit = first_that_fails(kBins, [&](int i) { return sh.first.count[i] <= (uint32_t)kList; }) - 1;
-    if (fit < 0) return;
+    if (fit < 0 || (wanted && fit < b)) return;
     list(bins_of(GATHER, 0, min(b, fit)), 0);
     list_lo = 0, list_hi = min(b, fit);
   }
@@ -469,10 +473,10 @@ struct Row {
   // a key of at least arg (no token). There is such a place: arg is within the row's sums.
   __device__ Place find(Kind kind, uint64_t arg) {
     if (listed(kind, arg)) return in_list(kind, arg, 0, 0);
-    need_masses();
     const Bins &s = sh.first;
-    const int b = kind == KEY ? bin_of(logit_of((uint32_t)arg), top, bin_scale)
-                              : kind == COUNT ? bin_of_count(arg) : first_that_fails(kBins, [&](int i) { return s.mass[i] < arg; });
+    int b = kind == KEY ? bin_of(logit_of((uint32_t)arg), top, bin_scale) : kind == COUNT ? bin_of_count(arg) : -1;
+    need_masses(b < 0 ? (masses_hi < 0 ? kBins : masses_hi) : b);
+    if (b < 0) b = min(first_that_fails(kBins, [&](int i) { return s.mass[i] < arg; }), masses_hi);
     const uint32_t count = b ? s.count[b - 1] : 0;
     const uint64_t mass = b ? s.mass[b - 1] : 0;
     if (b < list_lo || b > list_hi) {
@@ -482,9 +486,10 @@ struct Row {
     }
     return in_list(kind, arg, list_lo ? s.count[list_lo - 1] : 0, list_lo ? s.mass[list_lo - 1] : 0);
   }
-  __device__ void need_masses() {
-    if (!masses) command(Command{MASSES});
-    masses = true;
+  __device__ void need_masses(int b) {
+    if (masses_hi >= b) return;
+    command(bins_of(MASSES, 0, b));
+    masses_hi = b;
   }
 
   __device__ Place in_list(Kind kind, uint64_t arg, uint32_t count, uint64_t mass) {
@@ -619,7 +624,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   me.top = top, me.scale = weight_scale(temp > 0.f ? temp : 1.f);
   const bool sum_all = k <= 0 && (limit < 1.f || !(least_p > 0.f));  // whether the limits begin with the sum of all weights
-  me.bin_scale = fminf(me.scale.hi * (kBins / (sum_all ? kLong : kShort)), 3e38f);
+  const float range = k > 0 ? kRangeOfK : kRangeOfSum;
+  const int near = (int)(kBins * kNear / range);
+  me.bin_scale = fminf(me.scale.hi * (kBins / range), 3e38f);
   int token = -1;
   float logprob = -CUDART_INF_F;
   if (top != -CUDART_INF_F && k == 1) {
@@ -656,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           if (b < kBins) {
             atomicAdd(&sh.bins.count[b], 1u);
             if (sum_all) me.add_mass(b, w[e]);
-            if (*reinterpret_cast<volatile int32_t *>(&sh.listed) < kList) {
+            if (b < near && *reinterpret_cast<volatile int32_t *>(&sh.listed) < kList) {
               const int at = atomicAdd(&sh.listed, 1);
               if (at < kList) sh.code[at] = code_of(v[e], t0 + i + e);
             }
@@ -668,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (sum_all) me.add_last(last);
       if (sum_all) me.template sum_bins<true, true>(sh.first);
       else me.template sum_bins<true, false>(sh.first);
-      me.masses = sum_all;
+      me.masses_hi = sum_all ? kBins : -1;
       if (cta == 0 && tid == 0) sh.first.count[kBins] = (uint32_t)p.vocab;  // (the last bin is not counted)
       if (cta == 0) __syncthreads();
     }
@@ -677,14 +684,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const float least = least_p < 1.f ? sh.least : top;
       const int least_bin = has_min && least_p <= 1.f ? bin_of(least, top, me.bin_scale) : kBins;
       const bool all_k = !has_k || k >= p.vocab;
-      me.list_first(!all_k ? min(me.bin_of_count((uint64_t)k), kBins - 1) : has_min && !has_p ? min(least_bin, kBins - 1) : kBins - 1);
+      const int k_bin = all_k ? kBins : me.bin_of_count((uint64_t)k);
+      if (!all_k) me.list_first(k_bin, true, near);
+      else if (has_min && !has_p) me.list_first(least_bin, true, near);
+      else me.list_first(kBins - 1, false, near);
       uint64_t kept = ~0ull;
       if (sum_all) {
         kept = sh.first.mass[kBins];
       } else if (!all_k) {
         kept = me.find(Row<DT>::COUNT, (uint64_t)k).mass;
       } else if (has_p || least_bin == kBins) {
-        me.need_masses();
+        me.need_masses(kBins);
         kept = sh.first.mass[kBins];
       }
       if (has_p) {
@@ -693,7 +703,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       if (has_min) {
         uint64_t above = kWeightOne;  // at least the first token
-        if (least_p <= 1.f) above = max(me.find(Row<DT>::KEY, key_of(least + 0.f)).mass, kWeightOne);
+        if (least_p <= 1.f && least_bin > k_bin) above = kept;
+        else if (least_p <= 1.f) above = max(me.find(Row<DT>::KEY, key_of(least + 0.f)).mass, kWeightOne);
         kept = min(kept, above);
       }
       const float u = p.uniform[row];

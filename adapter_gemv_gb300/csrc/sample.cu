@@ -738,12 +738,17 @@ constexpr int kMaxSmem = 227 * 1024;
 
 template <int DT>
 cudaError_t launch(const mlora_sampling &p, int32_t *status, cudaStream_t stream) {
-  // Two CTAs an SM, as far as the rows leave it and the stretches stay long
+  // Stretches of at most 16384 tokens, unless that makes more than eight CTAs for an SM; more CTAs where the rows leave SMs without two.
+  // 256 x 128001 with 1, 2, 4, 8 CTAs a row: 436, 290, 267, 290 us; 256 x 32000 100, 85, 100, 139; 64 x 60000 150, 73, 59, 61; 1 x 32000 23,
+  // 19, 15, 13.
   int ctas = 1;
-  while (ctas < kMaxCtas && (int64_t)p.num_rows * ctas * 2 <= 2 * sm_count() && p.vocab >= 2048 * ctas) ctas *= 2;
+  const int64_t sms = sm_count();
+  while (ctas < kMaxCtas && ((p.vocab > 16384 * ctas && (int64_t)p.num_rows * ctas * 2 <= 8 * sms) ||
+                             ((int64_t)p.num_rows * ctas * 2 <= 2 * sms && p.vocab >= 2048 * ctas)))
+    ctas *= 2;
   const int stretch = ((p.vocab + ctas - 1) / ctas + 7) & ~7;
   // held in shared memory where that does not cost CTAs their SM, read again (from L2, mostly) where it does
-  const bool hold = smem_bytes(stretch) <= (((int64_t)p.num_rows * ctas > sm_count()) ? kMaxSmem / 2 - 1024 : kMaxSmem);
+  const bool hold = smem_bytes(stretch) <= (((int64_t)p.num_rows * ctas > sms) ? kMaxSmem / 2 - 1024 : kMaxSmem);
   const size_t smem = hold ? smem_bytes(stretch) : smem_bytes(0) + kRing * kThreads * 16;
   cudaError_t e = raise_smem<sample_kernel<DT>>(kMaxSmem);
   if (e != cudaSuccess) return e;

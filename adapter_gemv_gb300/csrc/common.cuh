@@ -214,16 +214,6 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
   }
 }
 
-// The same waits in loops that are short of registers: bounded by a number of polls (some 50 cycles each, or longer where
-// try_wait suspends: half a second and more), with no clock to read.
-constexpr uint32_t kWaitPolls = 1u << 24;
-__device__ __forceinline__ bool mbar_wait_polls(uint64_t *bar, uint32_t parity) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < kWaitPolls; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return false;
-}
-
 // ---- programmatic dependent launch -------------------------------------------------------------
 
 // Allow the next kernel in the stream to be scheduled now (it still waits for this grid to

@@ -9,14 +9,14 @@
 //
 // Few rows: W is read once, from memory, and that bounds. W's rows are the MMA's 128, x's its 16, 32 or 64 columns, so a product
 // is read back with 16 to 64 values a lane. The K blocks of a tile are split over a cluster of up to 8 CTAs, which add
-// their sums through distributed shared memory in rank order. 32 x 4096 x 22016 (90 MB): 18.2 us, 5.0 TB/s (20 SMs of 152
-// have two tiles); 8 x 8192 x 28672 37.6 us, 6.3 TB/s; 1 x 4096 x 4096 5.3 us.
+// their sums through distributed shared memory in rank order. 32 x 4096 x 22016 (92 MB): 17.7 us, 5.2 TB/s (20 SMs of 152
+// have two tiles); 8 x 8192 x 28672 37.6 us, 6.3 TB/s; 1 x 4096 x 4096 5.7 us.
 //
 // Many rows: 128 of x by up to 256 of W, one persistent CTA an SM. 12604 x 5120 x 13824: 808 us, 2.2 PFLOP/s; bound by the
 // sums: a tile's block is 32768 of them, 256 cycles of the SM's FMA units at least, and with the reads from TMEM, the scales and the
-// turns of the two accumulators 1000, where its MMAs take 512 (without the FMAs: 580 us). Tried there: a pair of CTAs on 256 rows
-// (cta_group::2, half the loads of W) 3 % slower; four accumulators of 128 columns 15 %; the next turn's barrier polled
-// early 6 %; eight warps of 128 sums a thread or loads of 16 and 32 columns at a time 20 to 45 %, by spills or without overlap.
+// turns of the two accumulators 1000, where its MMAs take 512. Tried on 7680 x 8192 x 7680 (353 us): a pair of CTAs on 256 rows
+// (cta_group::2, half the loads of W) 4 % slower; four accumulators of 128 columns 17 %; the next turn's barrier polled
+// early 6 %; loads of 16 and 32 columns at a time spill and are slower.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
     Turn turn;
     for (int i = 0; i < n_blocks; ++i, turn.next(p.stages)) {
       const int s = turn.at;
-      if (!mbar_wait_polls(&sh.empty[s], turn.odd ^ 1u)) {
+      if (!tc::mbar_wait_polls(&sh.empty[s], turn.odd ^ 1u)) {
         gone = true;
         break;
       }
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
     Turn turn, buf;
     for (int i = 0; i < n_blocks; ++i, turn.next(p.stages), buf.next(kBufs)) {
       const int s = turn.at;
-      if (!mbar_wait_polls(&sh.taken[buf.at], buf.odd ^ 1u) || !mbar_wait_polls(&sh.full[s], turn.odd)) {
+      if (!tc::mbar_wait_polls(&sh.taken[buf.at], buf.odd ^ 1u) || !tc::mbar_wait_polls(&sh.full[s], turn.odd)) {
         gone = true;
         break;
       }
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
       for (int k = 0; k < kChunk; ++k)
         if (i < NT && b + k < n_blocks) v[k] = sx[b + k];
       const float w = i < kChunk && b + i < n_blocks ? sw[b + i] : 0.f;
-      if (!mbar_wait_polls(&sh.used[chunk.at], chunk.odd ^ 1u)) {
+      if (!tc::mbar_wait_polls(&sh.used[chunk.at], chunk.odd ^ 1u)) {
         sh.late = 1;
         break;
       }
@@ -217,10 +217,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
     for (int j = 0; j < NT; ++j) acc[j] = 0.f;
     Turn buf, chunk;
     for (int i = 0; i < n_blocks; ++i) {
-      if (i % kChunk == 0 && !mbar_wait_polls(&sh.scaled[chunk.at], chunk.odd)) gone = true;
+      if (i % kChunk == 0 && !tc::mbar_wait_polls(&sh.scaled[chunk.at], chunk.odd)) gone = true;
       const float *sx = sh.sx[chunk.at * kChunk + i % kChunk];
       const float sw = sh.sw[chunk.at * kChunk + i % kChunk];
-      if (gone || !mbar_wait_polls(&sh.ready[buf.at], buf.odd)) {
+      if (gone || !tc::mbar_wait_polls(&sh.ready[buf.at], buf.odd)) {
         gone = true;
         break;
       }
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_rows_kernel(const __grid
       const int x0 = m * kTile, w0 = n * p.cols;
       for (int b = 0; b < p.blocks; ++b, turn.next(p.stages)) {
         const int s = turn.at;
-        if (!mbar_wait_polls(&sh.empty[s], turn.odd ^ 1u)) {
+        if (!tc::mbar_wait_polls(&sh.empty[s], turn.odd ^ 1u)) {
           gone = true;
           break;
         }
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_rows_kernel(const __grid
     for (int t = blockIdx.x; t < tiles && !gone; t += gridDim.x) {
       for (int b = 0; b < p.blocks; ++b, turn.next(p.stages), acc.next(2)) {
         const int s = turn.at;
-        if (!mbar_wait_polls(&sh.taken[acc.at], acc.odd ^ 1u) || !mbar_wait_polls(&sh.full[s], turn.odd)) {
+        if (!tc::mbar_wait_polls(&sh.taken[acc.at], acc.odd ^ 1u) || !tc::mbar_wait_polls(&sh.full[s], turn.odd)) {
           gone = true;
           break;
         }
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_rows_kernel(const __grid
           vb[k] = b + k < p.blocks ? xb[b + k] : 0.f;
         }
         const float w = b + i / 8 < p.blocks ? wa[b + i / 8] : 0.f;
-        if (!mbar_wait_polls(&sh.used[chunk.at], chunk.odd ^ 1u)) {
+        if (!tc::mbar_wait_polls(&sh.used[chunk.at], chunk.odd ^ 1u)) {
           gone = true, sh.late = 1;
           break;
         }
@@ -464,13 +464,13 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_rows_kernel(const __grid
       for (int j = 0; j < 64; ++j) acc[j] = 0.f;
       for (int b = 0; b < p.blocks; ++b) {
         if (b % kChunk == 0) {
-          if (!mbar_wait_polls(&sh.scaled[chunks & 1], (chunks >> 1) & 1)) gone = true;
+          if (!tc::mbar_wait_polls(&sh.scaled[chunks & 1], (chunks >> 1) & 1)) gone = true;
           ++chunks;
         }
         const int place = (int)((chunks - 1) & 1) * kChunk + b % kChunk;
         const float fx = lds_f32(scale + place * kTile * 4);
         const float f0 = fx * lds_f32(wscale + place * (kMaxCols / 8)), f1 = fx * lds_f32(wscale + place * (kMaxCols / 8) + 4);
-        if (gone || !mbar_wait_polls(&sh.ready[done & 1], (done >> 1) & 1)) {
+        if (gone || !tc::mbar_wait_polls(&sh.ready[done & 1], (done >> 1) & 1)) {
           gone = true, sh.late = 1;
           break;
         }

@@ -6,13 +6,21 @@
 // few: they serve the next limits, too) are gathered, sorted and summed. Weights and sums are whole numbers
 // (sample_weight.cuh), so that the atomics' order does not matter.
 //
-// A cluster of 1 to 8 CTAs takes a row, each a stretch of its vocabulary, which it reads once and holds as fp32 in shared
-// memory. The first CTA does the searching; the others count, reduce and gather for it: it writes a command into
-// its shared memory, and all meet at the cluster's barrier before and behind its execution.
+// A cluster of 1 to 8 CTAs takes a row, each a stretch of its vocabulary: held as fp32 in shared memory where that fits, else
+// streamed through a ring of cp.async for each pass (two CTAs an SM, so that one row's chain hides another's). The first CTA does
+// the searching; the others count, reduce and gather for it: it writes a command into its shared memory, and all meet at the
+// cluster's barrier before and behind its execution.
 //
-// Few tokens have a weight above 2^-12 of the largest, so that only those go to the histogram, with two atomics each; the
-// others are summed in registers and are one last bin. A bin of more than kList tokens, that one or one of many near or
-// equal logits, is divided again by the logits' bits, as often as it takes; equal logits are counted by their ids.
+// The bins cover kRangeOfK log2 units with top_k and kRangeOfSum where the sum of all weights is asked for; smaller weights are
+// one last bin, summed in registers. Tokens within kNear units of the largest are listed as they are counted: in
+// most rows that list answers everything. With top_k the weights are worked out up to the bin of the k-th token only. A bin of
+// more than kList tokens, one of many near or equal logits, is divided again by the logits' bits, as often as it
+// takes; equal logits are counted by their ids.
+//
+// One row of 32000: 13.5 us, the chain of loads, meetings and a sort. 256 rows of 128001 fp32 logits: 268 us (131 MB would be
+// 19 us of memory), bound by the weights of rows that need every token's, shared-memory atomics and the chain of each
+// row. Measured there: 1, 2, 4, 8 CTAs a row 436, 290, 267, 290 us; sums kept as three 32-bit parts instead of 64-bit atomics 450
+// against 434 us.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>

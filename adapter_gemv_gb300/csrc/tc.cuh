@@ -28,6 +28,18 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// ---- waits -----------------------------------------------------------------------------------------
+
+// A wait in a loop that is short of registers: bounded by a number of polls (some 50 cycles each, or longer where
+// try_wait suspends: half a second and more), with no clock to read.
+constexpr uint32_t kWaitPolls = 1u << 24;
+__device__ __forceinline__ bool mbar_wait_polls(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitPolls; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
 // ---- TMA -------------------------------------------------------------------------------------
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *m) {
@@ -212,5 +224,6 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[8]) {
                :
                : "memory");
 }
+
 }  // namespace tc
 }  // namespace mlora

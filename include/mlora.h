@@ -561,7 +561,8 @@ MLORA_API int lora_fp8_matmul(const mlora_matmul *args, int32_t *dev_status, voi
  * then has no part (T = 1). Behind lora_logits_adjust, the temperature is given to one of the two calls.
  * A NaN logit counts as -inf; -inf has w = 0; of logits of +inf each has w = 1 and all others 0. A row with nothing but
  * -inf gets token -1 and logprob -inf. uniform outside [0, 1) is taken to the nearer end, NaN as 0.
- * The sums are of whole numbers, 2^-44 of the largest w each (w to 2^-36 of itself): the same bits on every call.
+ * The sums are of whole numbers, 2^-44 of the largest w each (w to 2^-36 of itself, below 2^-18
+ * of the largest to 2^-40 of that): the same bits on every call.
  * Status: row_request[i] outside [-1, num_requests) (BAD_REQUEST): the row is skipped. */
 typedef struct {
   int32_t num_rows, vocab, dtype; /* 1 <= vocab <= MLORA_SAMPLE_MAX_VOCAB; dtype: MLORA_FP32, MLORA_BF16 or MLORA_FP16 */

@@ -197,3 +197,32 @@ def test_no_rows_launch_nothing(dev):  # noqa: F811
     before = m.launch_count()
     m.lora_sample(torch.empty(0, dtype=torch.int32, device=dev), torch.empty((0, 50), device=dev), torch.empty(0, device=dev))
     assert m.launch_count() == before
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_many_rows_of_a_large_vocabulary(dev, dtype):  # noqa: F811
+    """Rows that are read again instead of held, at odd addresses: peaked, flat, of few values, of one value, of -inf, with
+    each of the limits and none."""
+    rows, vocab = 160, 128001
+    g = torch.Generator(device=dev).manual_seed(17)
+    wide = torch.empty((rows, vocab + 5), device=dev).normal_(0, 2.5, generator=g)
+    wide[:, 1000:1040] += 10
+    wide[5::10] *= 0.01
+    wide[6::10] = wide[6::10].round()
+    wide[7::20] = 1.25
+    wide[8::20, 3:] = float("-inf")
+    wide[9::20] *= 40
+    wide[3, :] = float("-inf")
+    x = wide.to(dtype)[:, 3:vocab + 3]
+    c = torch.Generator().manual_seed(18)
+    u, kw = torch.rand(rows, generator=c), limits(rows, vocab, c)
+    kw["top_k"][::3] = kw["top_k"][::3].clamp(max=60)
+    kw["temperature"][::11] = 0
+    token, lp = torch.empty(rows, dtype=torch.int32, device=dev), torch.empty(rows, device=dev)
+    m.lora_sample(token, x, u.to(dev), logprob=lp, **{k: v.to(dev) for k, v in kw.items()})
+    want, want_lp, margin = ref.sample(x, u, **kw)
+    bad = [i for i in range(rows) if int(token[i]) != want[i] and margin[i] > 2.0 ** -30]
+    assert not bad and sum(t > 2.0 ** -30 for t in margin) > rows - 5, (bad, [want[i] for i in bad], token[bad].tolist())
+    near = torch.tensor(want_lp)
+    fine = torch.isfinite(near)
+    assert ((lp.cpu().double() - near).abs()[fine] <= 12 * ref.U * (1 + near.abs()[fine])).all()

@@ -171,7 +171,8 @@ class Sample(_StatusCall):
         rows, vocab = (int(i) for i in logits.shape)
         self.keep = (token, logits, uniform, row_request, temperature, top_k, top_p, min_p, logprob, status)
         lists = [t for t in (temperature, top_k, top_p, min_p) if t is not None]
-        n = int(lists[0].numel()) if lists else rows
+        # (without such arrays a request has nothing that its number could miss)
+        n = int(lists[0].numel()) if lists else rows if row_request is None else 2 ** 31 - 1
         if row_request is None and n < rows:
             raise ValueError(f"{rows} rows for {n} requests: give row_request")
         s = self.struct = mlora_sampling()

@@ -132,3 +132,12 @@ def test_sizes_of_the_header_and_the_binding():
     for name, value in (("MLORA_FP8_BLOCK", step.FP8_BLOCK), ("MLORA_ROW_MAX_WIDTH", step.ROW_MAX_WIDTH),
                         ("MLORA_SAMPLE_MAX_VOCAB", step.SAMPLE_MAX_VOCAB)):
         assert int(re.search(rf"#define {name} (\d+)", src).group(1)) == value
+
+
+def test_requests_without_limits_have_any_number(host_tensors):  # noqa: F811
+    """A row of request 5 in a call of one row: no array of the requests that it could be outside of."""
+    x, token, one = torch.zeros(1, 16), torch.zeros(1, dtype=torch.int32), torch.zeros(1)
+    request = torch.tensor([5], dtype=torch.int32)
+    assert m.Sample(token, x, one, row_request=request).struct.num_requests > 5
+    assert m.Sample(token, x, one, row_request=request, temperature=torch.ones(3)).struct.num_requests == 3
+    assert m.Sample(token, x, one).struct.num_requests == 1

@@ -536,7 +536,8 @@ MLORA_API int lora_quantize(const mlora_quant *args, void *stream);
  *     x_scale[i][b] * w_scale[n / 128][b] * sum over k in b of x[i][k] w[n][k] ),
  * the base product that lora_sgmv and lora_bgmv then add to. x: 8-bit rows; w: e4m3 [d_out][ldw >= d_in], the layout
  * (out_features, in_features), with a scale for every block of 128 x 128. A block's products are summed by the tensor
- * cores in fp32, the blocks in fp32 in a fixed order: the same call gives the same bits. y is no other array.
+ * cores in fp32, the blocks in fp32 in a fixed order: the same call gives the same bits. The two scales are multiplied first, in
+ * fp32, whose range their product must not leave. y is no other array.
  * TIMEOUT as for the adapters' calls. */
 typedef struct {
   int32_t num_rows, d_in, d_out, dtype; /* d_in a multiple of 16, d_out of 8 and below 2^31 - 256 */

@@ -12,7 +12,7 @@
 // their sums through distributed shared memory in rank order. 32 x 4096 x 22016 (92 MB): 17.7 us, 5.2 TB/s (20 SMs of 152
 // have two tiles); 8 x 8192 x 28672 37.6 us, 6.3 TB/s; 1 x 4096 x 4096 5.7 us.
 //
-// Many rows: 128 of x by up to 256 of W, one persistent CTA an SM. 12604 x 5120 x 13824: 808 us, 2.2 PFLOP/s; bound by the
+// Many rows: 128 of x by up to 256 of W, one persistent CTA an SM. 12604 x 5120 x 13824: 808 to 823 us, 2.2 PFLOP/s; bound by the
 // sums: a tile's block is 32768 of them, 256 cycles of the SM's FMA units at least, and with the reads from TMEM, the scales and the
 // turns of the two accumulators 1000, where its MMAs take 512. Tried on 7680 x 8192 x 7680 (353 us): a pair of CTAs on 256 rows
 // (cta_group::2, half the loads of W) 4 % slower; four accumulators of 128 columns 17 %; the next turn's barrier polled

@@ -27,7 +27,7 @@ __device__ __forceinline__ float block_scale(const float (&v)[8]) {
   for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(v[i]));
 #pragma unroll
   for (int d = kBlockChunks / 2; d; d >>= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, d));
-  return max_nan(m * (1.f / kFp8Max), kScaleMin);
+  return max_nan(m / kFp8Max, kScaleMin);
 }
 
 // v / scale as 8 e4m3 values. By the reciprocal, itself rounded once: a value within 2^-23 of itself of the border between

@@ -2,7 +2,7 @@
 //
 // Elementwise but for the maximum of each block of 128, which half a warp holds: every element read once and
 // written once, bound by memory; by launch and one load for a decode step's rows. silu(gate) x of 12604 x 13824 with 16 and 8
-// bits out: 279 us, 4.4 TB/s. With __expf and __fdividef it took 205, but more values went to the wrong one of two e4m3
+// bits out: 279 us, 4.4 TB/s. With __expf and __fdividef it took 205, with expf and __fdividef 225, but more values went to the wrong one of two e4m3
 // neighbours than with fp32's exponential and quotient.
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -326,7 +326,7 @@ def lora_set_programmatic_launch(enable: bool) -> bool:
 
 
 def lora_test_set_wait_limit_ns(limit_ns: int) -> None:
-    """Testing hook: time limit of the CUDA-core kernels' waits for this thread's later calls
+    """Testing hook: time limit of the CUDA-core kernels' and the 8-bit product's waits for this thread's later calls
     (0 = the default). Only the tests of the time-out path use it."""
     lib().lora_test_set_wait_limit_ns(int(limit_ns))
 

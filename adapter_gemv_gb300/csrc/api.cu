@@ -37,6 +37,7 @@ int cuda_fail(cudaError_t e, const char *where) {
 // The same error text and launch count for the entry points of serve_api.cu.
 int mlora::api_cuda_fail(cudaError_t e, const char *where) { return cuda_fail(e, where); }
 void mlora::api_count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+uint64_t mlora::api_wait_limit_ns() { return g_wait_limit_ns; }
 
 namespace {
 

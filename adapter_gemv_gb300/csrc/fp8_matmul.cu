@@ -40,6 +40,7 @@ struct MatmulParams {
   int32_t cols;            // many rows: W's rows of a tile
   int32_t split;           // few rows: CTAs that share a tile's blocks
   int32_t stages;
+  uint64_t wait_ns;        // limit of a wait
 };
 
 __device__ __forceinline__ float4 dsmem_ld_f32x4(uint32_t addr) {
@@ -74,10 +75,16 @@ struct Turn {
   }
 };
 
-// Waits until what is on its way into shared memory has had time to land, in a CTA that gave up.
-__device__ __forceinline__ void let_land() {
-  const uint64_t t0 = global_timer_ns();
-  while (global_timer_ns() - t0 < kDrainLimitNs) __nanosleep(1000);
+// Behind its last load, the warp of loads waits until all have landed, whichever warp gave up before it used them: a CTA ends
+// with none on its way. `turn`: the next load's; a stage that had none is through its wait at once.
+__device__ __forceinline__ void drain_loads(uint64_t *full, const Turn &turn, int stages) {
+  for (int s = 0; s < stages; ++s) (void)tc::mbar_wait_warp<false>(&full[s], s < turn.at ? turn.odd : turn.odd ^ 1u, kDrainLimitNs);
+}
+// The same of the warp of MMAs: none is at work on shared memory or TMEM when the CTA gives them up.
+__device__ __forceinline__ void drain_mmas(uint64_t *drained) {
+  if (tc::elect_one()) tc::mma_commit(drained);
+  __syncwarp();
+  (void)tc::mbar_wait_warp<false>(drained, 0, kDrainLimitNs);
 }
 
 // ---- few rows: 128 rows of W (the MMA's M) by NT rows of x ----------------------------------------------------
@@ -100,7 +107,7 @@ struct FewHead {
   float sw[2 * kChunk];
 };
 
-template <int DT, int NT>
+template <int DT, int NT, bool SHORT>
 __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_constant__ MatmulParams p,
                                                                   const __grid_constant__ CUtensorMap map_x,
                                                                   const __grid_constant__ CUtensorMap map_w, int32_t *status) {
@@ -144,7 +151,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
     Turn turn;
     for (int i = 0; i < n_blocks; ++i, turn.next(p.stages)) {
       const int s = turn.at;
-      if (!tc::mbar_wait_polls(&sh.empty[s], turn.odd ^ 1u)) {
+      if (!tc::mbar_wait_warp<SHORT>(&sh.empty[s], turn.odd ^ 1u, p.wait_ns)) {
         gone = true;
         break;
       }
@@ -155,16 +162,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
       }
       __syncwarp();
     }
-    if (gone) {
-      sh.late = 1;
-      let_land();
-    }
+    if (gone) sh.late = 1;
+    drain_loads(sh.full, turn, p.stages);
   } else if (warp == 5) {
     constexpr uint32_t idesc = tc::idesc_e4m3(kTile, NT);
     Turn turn, buf;
     for (int i = 0; i < n_blocks; ++i, turn.next(p.stages), buf.next(kBufs)) {
       const int s = turn.at;
-      if (!tc::mbar_wait_polls(&sh.taken[buf.at], buf.odd ^ 1u) || !tc::mbar_wait_polls(&sh.full[s], turn.odd)) {
+      if (!tc::mbar_wait_warp<SHORT>(&sh.taken[buf.at], buf.odd ^ 1u, p.wait_ns) || !tc::mbar_wait_warp<SHORT>(&sh.full[s], turn.odd, p.wait_ns)) {
         gone = true;
         break;
       }
@@ -180,14 +185,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
       }
       __syncwarp();
     }
-    if (gone) {
-      sh.late = 1;
-      if (tc::elect_one()) {
-        tc::mma_commit(&sh.drained);
-        (void)mbar_wait(&sh.drained, 0, kDrainLimitNs);
-      }
-      __syncwarp();
-    }
+    if (gone) sh.late = 1;
+    drain_mmas(&sh.drained);
   } else if (warp >= 6) {
     // scales, kChunk blocks at a time: thread i those of x's row i, and of W's rows block i of them
     const int i = tid - 6 * 32;
@@ -200,7 +199,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
       for (int k = 0; k < kChunk; ++k)
         if (i < NT && b + k < n_blocks) v[k] = sx[b + k];
       const float w = i < kChunk && b + i < n_blocks ? sw[b + i] : 0.f;
-      if (!tc::mbar_wait_polls(&sh.used[chunk.at], chunk.odd ^ 1u)) {
+      if (!tc::mbar_wait_warp<SHORT>(&sh.used[chunk.at], chunk.odd ^ 1u, p.wait_ns)) {
         sh.late = 1;
         break;
       }
@@ -217,14 +216,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
     for (int j = 0; j < NT; ++j) acc[j] = 0.f;
     Turn buf, chunk;
     for (int i = 0; i < n_blocks; ++i) {
-      if (i % kChunk == 0 && !tc::mbar_wait_polls(&sh.scaled[chunk.at], chunk.odd)) gone = true;
+      if (i % kChunk == 0 && !tc::mbar_wait_warp<SHORT>(&sh.scaled[chunk.at], chunk.odd, p.wait_ns)) gone = true;
       const float *sx = sh.sx[chunk.at * kChunk + i % kChunk];
       const float sw = sh.sw[chunk.at * kChunk + i % kChunk];
-      if (gone || !tc::mbar_wait_polls(&sh.ready[buf.at], buf.odd)) {
+      if (gone || !tc::mbar_wait_warp<SHORT>(&sh.ready[buf.at], buf.odd, p.wait_ns)) {
         gone = true;
         break;
       }
-      __syncwarp();
       tc::tc_fence_after();
       const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(buf.at * NT);
       // 8 columns are added while the next 8 are on their way
@@ -327,7 +325,7 @@ __device__ __forceinline__ void tile_at(const MatmulParams &p, int t, int &m, in
   m = band * kBand + in - n * height;
 }
 
-template <int DT>
+template <int DT, bool SHORT>
 __global__ void __launch_bounds__(kManyThreads, 1) many_rows_kernel(const __grid_constant__ MatmulParams p,
                                                                     const __grid_constant__ CUtensorMap map_x,
                                                                     const __grid_constant__ CUtensorMap map_w, int32_t *status) {
@@ -370,7 +368,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_rows_kernel(const __grid
       const int x0 = m * kTile, w0 = n * p.cols;
       for (int b = 0; b < p.blocks; ++b, turn.next(p.stages)) {
         const int s = turn.at;
-        if (!tc::mbar_wait_polls(&sh.empty[s], turn.odd ^ 1u)) {
+        if (!tc::mbar_wait_warp<SHORT>(&sh.empty[s], turn.odd ^ 1u, p.wait_ns)) {
           gone = true;
           break;
         }
@@ -383,10 +381,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_rows_kernel(const __grid
         __syncwarp();
       }
     }
-    if (gone) {
-      sh.late = 1;
-      let_land();
-    }
+    if (gone) sh.late = 1;
+    drain_loads(sh.full, turn, p.stages);
   } else if (warp == 17) {
     const uint32_t idesc = tc::idesc_e4m3(kTile, p.cols);
     Turn turn, acc;
@@ -394,7 +390,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_rows_kernel(const __grid
     for (int t = blockIdx.x; t < tiles && !gone; t += gridDim.x) {
       for (int b = 0; b < p.blocks; ++b, turn.next(p.stages), acc.next(2)) {
         const int s = turn.at;
-        if (!tc::mbar_wait_polls(&sh.taken[acc.at], acc.odd ^ 1u) || !tc::mbar_wait_polls(&sh.full[s], turn.odd)) {
+        if (!tc::mbar_wait_warp<SHORT>(&sh.taken[acc.at], acc.odd ^ 1u, p.wait_ns) || !tc::mbar_wait_warp<SHORT>(&sh.full[s], turn.odd, p.wait_ns)) {
           gone = true;
           break;
         }
@@ -411,13 +407,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_rows_kernel(const __grid
         __syncwarp();
       }
     }
-    if (gone) {
-      sh.late = 1;
-      if (tc::elect_one()) {
-        tc::mma_commit(&sh.drained);
-        (void)mbar_wait(&sh.drained, 0, kDrainLimitNs);
-      }
-    }
+    if (gone) sh.late = 1;
+    drain_mmas(&sh.drained);
   } else if (warp >= 18) {
     // scales, kChunk blocks at a time, so that the sums read them from shared memory: from global memory, a row of x a
     // lane, they would be 32 sectors for each of 16 warps and every block
@@ -439,7 +430,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_rows_kernel(const __grid
           vb[k] = b + k < p.blocks ? xb[b + k] : 0.f;
         }
         const float w = b + i / 8 < p.blocks ? wa[b + i / 8] : 0.f;
-        if (!tc::mbar_wait_polls(&sh.used[chunk.at], chunk.odd ^ 1u)) {
+        if (!tc::mbar_wait_warp<SHORT>(&sh.used[chunk.at], chunk.odd ^ 1u, p.wait_ns)) {
           gone = true, sh.late = 1;
           break;
         }
@@ -464,17 +455,16 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_rows_kernel(const __grid
       for (int j = 0; j < 64; ++j) acc[j] = 0.f;
       for (int b = 0; b < p.blocks; ++b) {
         if (b % kChunk == 0) {
-          if (!tc::mbar_wait_polls(&sh.scaled[chunks & 1], (chunks >> 1) & 1)) gone = true;
+          if (!tc::mbar_wait_warp<SHORT>(&sh.scaled[chunks & 1], (chunks >> 1) & 1, p.wait_ns)) gone = true;
           ++chunks;
         }
         const int place = (int)((chunks - 1) & 1) * kChunk + b % kChunk;
         const float fx = lds_f32(scale + place * kTile * 4);
         const float f0 = fx * lds_f32(wscale + place * (kMaxCols / 8)), f1 = fx * lds_f32(wscale + place * (kMaxCols / 8) + 4);
-        if (gone || !tc::mbar_wait_polls(&sh.ready[done & 1], (done >> 1) & 1)) {
+        if (gone || !tc::mbar_wait_warp<SHORT>(&sh.ready[done & 1], (done >> 1) & 1, p.wait_ns)) {
           gone = true, sh.late = 1;
           break;
         }
-        __syncwarp();
         tc::tc_fence_after();
         const uint32_t at = lanes + (done & 1) * kMaxCols;
         // 8 columns are added while the next 8 are on their way (columns behind a narrower tile's are read as they are and not used)
@@ -534,7 +524,7 @@ bool encode_bytes(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DT, int NT>
+template <int DT, int NT, bool SHORT>
 cudaError_t launch_few(MatmulParams p, int32_t *status, cudaStream_t stream) {
   const mlora_matmul &a = p.a;
   p.nt = (a.d_out - 1) / kTile + 1;
@@ -543,15 +533,15 @@ cudaError_t launch_few(MatmulParams p, int32_t *status, cudaStream_t stream) {
   CUtensorMap map_x, map_w;
   if (!encode_bytes(&map_x, a.x, a.d_in, a.num_rows, a.ldx, NT) || !encode_bytes(&map_w, a.w, a.d_in, a.d_out, a.ldw, kTile))
     return cudaErrorInvalidValue;
-  cudaError_t e = raise_smem<few_rows_kernel<DT, NT>>(kFewSmem);
+  cudaError_t e = raise_smem<few_rows_kernel<DT, NT, SHORT>>(kFewSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)p.mt * p.nt * p.split));
-  e = launch_waiting(few_rows_kernel<DT, NT>, grid, dim3(kFewThreads), kFewSmem, p.split, stream, p, map_x, map_w, status);
+  e = launch_waiting(few_rows_kernel<DT, NT, SHORT>, grid, dim3(kFewThreads), kFewSmem, p.split, stream, p, map_x, map_w, status);
   if (e == cudaSuccess) api_count_launch();
   return e;
 }
 
-template <int DT>
+template <int DT, bool SHORT>
 cudaError_t launch_many(MatmulParams p, int32_t *status, cudaStream_t stream) {
   const mlora_matmul &a = p.a;
   p.nt = (a.d_out - 1) / p.cols + 1;
@@ -560,15 +550,16 @@ cudaError_t launch_many(MatmulParams p, int32_t *status, cudaStream_t stream) {
   CUtensorMap map_x, map_w;
   if (!encode_bytes(&map_x, a.x, a.d_in, a.num_rows, a.ldx, kTile) || !encode_bytes(&map_w, a.w, a.d_in, a.d_out, a.ldw, p.cols))
     return cudaErrorInvalidValue;
-  cudaError_t e = raise_smem<many_rows_kernel<DT>>(kManySmem);
+  cudaError_t e = raise_smem<many_rows_kernel<DT, SHORT>>(kManySmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(std::min(p.mt * p.nt, sm_count()));
-  e = launch_waiting(many_rows_kernel<DT>, grid, dim3(kManyThreads), kManySmem, 1, stream, p, map_x, map_w, status);
+  e = launch_waiting(many_rows_kernel<DT, SHORT>, grid, dim3(kManyThreads), kManySmem, 1, stream, p, map_x, map_w, status);
   if (e == cudaSuccess) api_count_launch();
   return e;
 }
 
-template <int DT>
+// SHORT: a limit of the waits that the caller has set.
+template <int DT, bool SHORT>
 cudaError_t dispatch(MatmulParams p, int32_t *status, cudaStream_t stream) {
   const int rows = p.a.num_rows, sms = sm_count();
   p.blocks = (p.a.d_in - 1) / kBlock + 1;
@@ -581,9 +572,9 @@ cudaError_t dispatch(MatmulParams p, int32_t *status, cudaStream_t stream) {
     // K split as long as every CTA has an SM to itself: 1 x 4096 x 4096 9.6, 6.9, 5.3, 5.6 us with 1, 2, 4, 8 (256 CTAs); 64 rows of
     // it 12.6, 9.3, 8.1, 11.5; 1 x 4096 x 1024 9.6, 6.8, 5.0, 4.3
     p.split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(kMaxSplit, p.blocks), sms / tiles));
-    if (nt == 16) return launch_few<DT, 16>(p, status, stream);
-    if (nt == 32) return launch_few<DT, 32>(p, status, stream);
-    return launch_few<DT, 64>(p, status, stream);
+    if (nt == 16) return launch_few<DT, 16, SHORT>(p, status, stream);
+    if (nt == 32) return launch_few<DT, 32, SHORT>(p, status, stream);
+    return launch_few<DT, 64, SHORT>(p, status, stream);
   }
   // The width of the tiles by what the SM with the most of them takes: a block of K takes 600 + columns (0.42 us with 128,
   // 0.45 with 192, 0.5 with 256). 1024 x 8192 x 28672 with 128, 192, 224, 256 columns: 326, 232, 209, 198 us; 213 x 8192 x 28672 85,
@@ -594,22 +585,25 @@ cudaError_t dispatch(MatmulParams p, int32_t *status, cudaStream_t stream) {
     const int64_t most = (mt * ((p.a.d_out - 1) / cols + 1) + sms - 1) / sms, cost = most * (600 + cols);
     if (cost < least) least = cost, p.cols = cols;
   }
-  return launch_many<DT>(p, status, stream);
+  return launch_many<DT, SHORT>(p, status, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_matmul(const mlora_matmul &a, int32_t *status, cudaStream_t stream) {
+cudaError_t launch_fp8_matmul(const mlora_matmul &a, int32_t *status, uint64_t wait_ns, cudaStream_t stream) {
   // rows of a launch: tiles of 16 rows by 128 are counted in 31 bits, eight times over
   const int64_t most = std::max<int64_t>(1, (INT32_MAX / kMaxSplit) / ((a.d_out - 1) / kTile + 1)) * 16;
   for (int64_t row0 = 0; row0 < a.num_rows; row0 += most) {
     MatmulParams p{};
     p.a = a;
+    p.wait_ns = wait_ns ? wait_ns : kWaitLimitNs;
     p.a.num_rows = (int32_t)std::min<int64_t>(most, a.num_rows - row0);
     p.a.x = static_cast<const uint8_t *>(a.x) + row0 * a.ldx;
     p.a.x_scale = a.x_scale + row0 * a.ldxs;
     p.a.y = static_cast<uint16_t *>(a.y) + row0 * a.ldy;
-    const cudaError_t e = a.dtype == MLORA_BF16 ? dispatch<MLORA_BF16>(p, status, stream) : dispatch<MLORA_FP16>(p, status, stream);
+    const auto run = a.dtype == MLORA_BF16 ? (wait_ns ? dispatch<MLORA_BF16, true> : dispatch<MLORA_BF16, false>)
+                                           : (wait_ns ? dispatch<MLORA_FP16, true> : dispatch<MLORA_FP16, false>);
+    const cudaError_t e = run(p, status, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -9,9 +9,11 @@
 
 namespace mlora {
 
-// Defined in api.cu: records a CUDA error's text and returns MLORA_ERR_CUDA; counts one launch.
+// Defined in api.cu: records a CUDA error's text and returns MLORA_ERR_CUDA; counts one launch; the limit of a kernel's
+// waits that this thread has set, 0: the kernels' default.
 int api_cuda_fail(cudaError_t e, const char *where);
 void api_count_launch();
+uint64_t api_wait_limit_ns();
 
 cudaError_t launch_kv_layout(const mlora_kv_batch &b, int32_t *status, cudaStream_t stream);
 cudaError_t launch_kv_append(const mlora_kv_cache &c, const mlora_kv_rows &r, int32_t layer, int32_t *status,
@@ -23,7 +25,7 @@ int64_t kv_attention_workspace_bytes(int32_t head_dim);
 cudaError_t launch_logits_adjust(const mlora_logits &a, int32_t *status, cudaStream_t stream);
 cudaError_t launch_rms_norm(const mlora_norm &a, cudaStream_t stream);
 cudaError_t launch_quantize(const mlora_quant &a, cudaStream_t stream);
-cudaError_t launch_fp8_matmul(const mlora_matmul &a, int32_t *status, cudaStream_t stream);
+cudaError_t launch_fp8_matmul(const mlora_matmul &a, int32_t *status, uint64_t wait_ns, cudaStream_t stream);
 cudaError_t launch_sample(const mlora_sampling &a, int32_t *status, cudaStream_t stream);
 
 // Defined in decode_launch.cu: number of SMs of the current device.

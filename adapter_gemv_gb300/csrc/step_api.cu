@@ -102,7 +102,7 @@ int lora_fp8_matmul(const mlora_matmul *a, int32_t *dev_status, void *stream) {
   TRY(check_rows(a->y, a->ldy, a->d_out));
   if (a->y == a->x || a->y == a->w) return MLORA_ERR_SHAPE;
   if (!aligned(dev_status, 4)) return MLORA_ERR_ALIGN;
-  return done(mlora::launch_fp8_matmul(*a, dev_status, static_cast<cudaStream_t>(stream)), "8-bit product launch");
+  return done(mlora::launch_fp8_matmul(*a, dev_status, mlora::api_wait_limit_ns(), static_cast<cudaStream_t>(stream)), "8-bit product launch");
 }
 
 int lora_sample(const mlora_sampling *a, int32_t *dev_status, void *stream) {

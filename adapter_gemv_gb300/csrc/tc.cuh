@@ -30,14 +30,26 @@ __device__ __forceinline__ bool elect_one() {
 
 // ---- waits -----------------------------------------------------------------------------------------
 
-// A wait in a loop that is short of registers: bounded by a number of polls (some 50 cycles each, or longer where
-// try_wait suspends: half a second and more), with no clock to read.
-constexpr uint32_t kWaitPolls = 1u << 24;
-__device__ __forceinline__ bool mbar_wait_polls(uint64_t *bar, uint32_t parity) {
+// A whole warp's wait of at most limit_ns. Each poll's end, and the wait's, is the warp's: should the limit fall on some lanes
+// first, all of them give up, so that the warp stays whole for what needs it whole (elect.sync, tcgen05.ld, __syncwarp).
+// The clock is read behind 2^14 polls of some 50 cycles: most waits end within a microsecond, and whatever stands before a
+// poll adds to them. 256 x 8192 x 28672 of the 8-bit product takes 62.9 us so, 65.5 with limit_ns looked at behind the first poll, 68.8 before
+// it (61.6 without votes and clock). So a limit that may be shorter than those polls is another variant, SHORT, without
+// them; its polls do not suspend the thread either.
+constexpr int kPollsBeforeClock = 1 << 14;
+template <bool SHORT>
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+  if constexpr (!SHORT) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < kWaitPolls; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return false;
+    for (int i = 0; i < kPollsBeforeClock; ++i)
+      if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+  }
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  for (;;) {
+    if (__all_sync(~0u, mbar_test(bar, parity))) return true;
+    if (__any_sync(~0u, global_timer_ns() - t0 > limit_ns)) return false;
+  }
 }
 
 // ---- TMA -------------------------------------------------------------------------------------

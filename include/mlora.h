@@ -604,8 +604,8 @@ MLORA_API int lora_abi_version(void);
 MLORA_API int64_t lora_launch_count(void);
 
 /* Testing hook for the time-out path: limit, in nanoseconds, of the waits inside the CUDA-core
- * kernels launched later by the calling thread (the waits for their own bulk copies and for
- * their cluster peers' partial sums). 0 restores the default of 2 s. With a limit of a few
+ * kernels and lora_fp8_matmul's launched later by the calling thread (the waits for their own bulk
+ * copies, for their cluster peers' partial sums and between a product's loads, MMAs and sums). 0 restores the default of 2 s. With a limit of a few
  * nanoseconds a wait gives up unless its data has already landed, the kernel sets
  * MLORA_STATUS_TIMEOUT and skips the work that needed the data, and copies still in flight are
  * drained (with the default limit) before the kernel exits. Not for production use: results of

@@ -486,7 +486,7 @@ MLORA_API int lora_logits_adjust(const mlora_logits *args, int32_t *dev_status, 
  * 8-bit rows: e4m3 values (1 sign, 4 exponent, 3 mantissa bits, largest 448) q [num_rows][ldq] with an fp32 scale for
  * every block of MLORA_FP8_BLOCK columns of a row (the last may be shorter), scale [num_rows][lds]; an element
  * stands for q * scale. Those of values v are
- *   scale = max(max |v| of the block / 448, 2^-126),   q = v / scale rounded to the nearest e4m3, ties to even;
+ *   scale = max(max |v| of the block / 448, 2^-126),   q = v / scale, in fp32, rounded to the nearest e4m3, ties to even;
  * a NaN makes its block's scale and values NaN, an infinity makes the scale an infinity, its own value NaN and the
  * others 0. The conventions above hold: pointers of 16-bit and 8-bit arrays 16-byte aligned, their widths and
  * leading dimensions multiples of 8 unless said, fp32 and int32 arrays 4-byte aligned. */

@@ -37,17 +37,19 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
   const int64_t row = blockIdx.x;
   const uint16_t *x = static_cast<const uint16_t *>(p.x) + row * p.ldx;
   const uint16_t *res = static_cast<const uint16_t *>(p.residual) + row * p.ldr;
-  float h[CH][8];
+  float h[CH][8];  // half of x + residual, which may pass fp32's range: halves of 16-bit numbers are exact, so is 2 h below it
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int e = (c * blockDim.x + threadIdx.x) * 8;
     if (e < p.width) {
       unpack8<DT>(ldg_u4(x + e), h[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[c][i] *= 0.5f;
       if (p.residual) {
         float r[8];
         unpack8<DT>(ldg_u4(res + e), r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[c][i] += r[i];
+        for (int i = 0; i < 8; ++i) h[c][i] = fmaf(0.5f, r[i], h[c][i]);
       }
     } else {
 #pragma unroll
@@ -60,7 +62,8 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(h[c][i], h[c][i], s);
   s = block_sum(s, part[0]);
-  float scale = 1.f, eps = p.eps;
+  float scale = 2.f, eps = p.eps;
+  s *= 4.f;
   if (isinf(s)) {  // squares beyond fp32's range (or an infinity in the row): summed as those of h 2^-72
     scale = 0x1p-72f, eps = 0.f;
     s = 0.f;
@@ -75,9 +78,12 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
   for (int c = 0; c < CH; ++c) {
     const int e = (c * blockDim.x + threadIdx.x) * 8;
     const bool in = e < p.width;
-    if (in && p.residual)
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.residual_out) + row * p.ldro + e) = pack8<DT>(h[c]);
     float v[8];
+    if (in && p.residual) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = h[c][i] + h[c][i];
+      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.residual_out) + row * p.ldro + e) = pack8<DT>(v);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = h[c][i] * scale * r;
     if (in && p.weight) {

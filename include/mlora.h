@@ -500,7 +500,8 @@ MLORA_API int lora_logits_adjust(const mlora_logits *args, int32_t *dev_status, 
  *   (q, q_scale) = v as 8-bit rows,
  * in fp32 from the unrounded h, each output rounded once. residual and residual_out come together, and q and q_scale; out
  * or q may be NULL, not both. residual_out may be residual or x, and out may be x or residual, with equal leading dimensions; no two
- * outputs are the same array. Squares that pass fp32's range are summed scaled: a finite row has finite results. */
+ * outputs are the same array. Sums and squares may pass fp32's range: finite rows of x and residual have a
+ * finite norm (residual_out is rounded as any sum is). */
 typedef struct {
   int32_t num_rows, width, dtype; /* width a multiple of 8, 8 .. MLORA_ROW_MAX_WIDTH; dtype of x, residual, weight, out */
   float eps;                      /* > 0, finite */

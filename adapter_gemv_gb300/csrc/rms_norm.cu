@@ -62,18 +62,17 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(h[c][i], h[c][i], s);
   s = block_sum(s, part[0]);
-  float scale = 2.f, eps = p.eps;
-  s *= 4.f;
-  if (isinf(s)) {  // squares beyond fp32's range (or an infinity in the row): summed as those of h 2^-72
-    scale = 0x1p-72f, eps = 0.f;
+  float scale = 2.f, mean = 4.f * s / (float)p.width + p.eps;
+  if (isinf(mean)) {  // squares, or eps, beyond fp32's range (or an infinity in the row): summed as those of h 2^-72
+    scale = 0x1p-72f;
     s = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s = fmaf(h[c][i] * scale, h[c][i] * scale, s);
-    s = block_sum(s, part[1]);
+    mean = block_sum(s, part[1]) / (float)p.width + p.eps * 0x1p-146f;  // (h is a half)
   }
-  const float r = 1.f / sqrtf(s / (float)p.width + eps);
+  const float r = 1.f / sqrtf(mean);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int e = (c * blockDim.x + threadIdx.x) * 8;

@@ -30,3 +30,13 @@ def test_sums_of_two_finite_rows_beyond_fp32(dev, width, in_place):  # noqa: F81
     ref.check_rows8(q, scale, v, rel, "q")
     ref.within(sums, h, ref.U, "residual")
     assert torch.isinf(sums[2]).all() and sums[0, 3] == float("inf") and sums[1, 0] == -float("inf") and sums[3, 5] == 0
+
+
+@pytest.mark.parametrize("eps", [1e25, 1e30, 1e38, 3.3e38])
+def test_an_eps_that_counts_beside_the_largest_squares(dev, eps):  # noqa: F811
+    x = normal((4, 264), BF16, dev, 4)
+    for i, size in enumerate((6e18, 1e19, 3e12, 1.0)):
+        x[i] = (x[i].float() * size).to(BF16)
+    out = torch.empty_like(x)
+    m.lora_rms_norm(x, None, eps, out=out)
+    ref.within(out, *ref.norm(x, None, None, eps)[1:], "out")

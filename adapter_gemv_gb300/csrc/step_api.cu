@@ -45,7 +45,7 @@ int lora_rms_norm(const mlora_norm *a, void *stream) {
   if (!a) return MLORA_ERR_NULL;
   TRY(check_type(a->dtype));
   if (a->num_rows < 0 || a->width < 8 || a->width > MLORA_ROW_MAX_WIDTH) return MLORA_ERR_SHAPE;
-  if (!(a->eps > 0.f) || !std::isfinite(a->eps)) return MLORA_ERR_SHAPE;
+  if (!(a->eps >= 0x1p-126f) || !std::isfinite(a->eps)) return MLORA_ERR_SHAPE;
   if (a->width % 8) return MLORA_ERR_ALIGN;
   if (a->num_rows == 0) return MLORA_OK;
   TRY(check_rows(a->x, a->ldx, a->width));

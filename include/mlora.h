@@ -504,7 +504,7 @@ MLORA_API int lora_logits_adjust(const mlora_logits *args, int32_t *dev_status, 
  * finite norm (residual_out is rounded as any sum is). */
 typedef struct {
   int32_t num_rows, width, dtype; /* width a multiple of 8, 8 .. MLORA_ROW_MAX_WIDTH; dtype of x, residual, weight, out */
-  float eps;                      /* > 0, finite */
+  float eps;                      /* at least 2^-126, finite */
   const void *x;                  /* [num_rows][ldx] */
   const void *residual;           /* [num_rows][ldr], or NULL */
   const void *weight;             /* [width], or NULL: 1 */

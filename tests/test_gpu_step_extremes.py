@@ -40,3 +40,16 @@ def test_an_eps_that_counts_beside_the_largest_squares(dev, eps):  # noqa: F811
     out = torch.empty_like(x)
     m.lora_rms_norm(x, None, eps, out=out)
     ref.within(out, *ref.norm(x, None, None, eps)[1:], "out")
+
+
+@pytest.mark.parametrize("eps", [2.0 ** -126, 1e-30])
+def test_the_smallest_eps(dev, eps):  # noqa: F811
+    """Rows whose squares are as small as eps, or leave fp32's range downwards: each square and their sums are off by
+    4 x 2^-150 at most, 2^-22 of the sum with eps, half of that behind the root."""
+    x = normal((5, 392), BF16, dev, 6)
+    for i, size in enumerate((2.0 ** -63, 2.0 ** -66, 2.0 ** -80, 2.0 ** -50, 0.0)):
+        x[i] = (x[i].float() * size).to(BF16)
+    out = torch.empty_like(x)
+    m.lora_rms_norm(x, None, eps, out=out)
+    _, v, rel = ref.norm(x, None, None, eps)
+    ref.within(out, v, rel + 2.0 ** -23, "out")

@@ -37,6 +37,12 @@ int check_q_out(const void *q, int64_t ldq, const float *scale, int64_t lds, int
   return check_scale(scale, lds, blocks_of(width));
 }
 
+// Whether an output (or none) is over no other of the call's arrays: a CTA would read there what another has written.
+template <class... P>
+bool apart(const void *out, const P *...others) {
+  return !out || ((static_cast<const void *>(others) != out) && ...);
+}
+
 }  // namespace
 
 extern "C" {
@@ -65,6 +71,9 @@ int lora_rms_norm(const mlora_norm *a, void *stream) {
   }
   TRY(check_q_out(a->q, a->ldq, a->q_scale, a->lds, a->width));
   if (!aligned(a->weight, 16)) return MLORA_ERR_ALIGN;
+  if (!apart(a->residual_out, a->weight) || !apart(a->out, a->weight) || !apart(a->q, a->x, a->residual, a->weight) ||
+      !apart(a->q_scale, a->x, a->residual, a->weight, a->residual_out, a->out, a->q))
+    return MLORA_ERR_SHAPE;
   return done(mlora::launch_rms_norm(*a, static_cast<cudaStream_t>(stream)), "norm launch");
 }
 
@@ -84,6 +93,7 @@ int lora_quantize(const mlora_quant *a, void *stream) {
     if (a->out == a->q) return MLORA_ERR_SHAPE;
   }
   TRY(check_q_out(a->q, a->ldq, a->q_scale, a->lds, a->width));
+  if (!apart(a->q, a->x, a->gate) || !apart(a->q_scale, a->x, a->gate, a->out, a->q)) return MLORA_ERR_SHAPE;
   return done(mlora::launch_quantize(*a, static_cast<cudaStream_t>(stream)), "quantize launch");
 }
 
@@ -100,7 +110,7 @@ int lora_fp8_matmul(const mlora_matmul *a, int32_t *dev_status, void *stream) {
   TRY(check_scale(a->x_scale, a->ldxs, blocks));
   TRY(check_scale(a->w_scale, a->ldws, blocks));
   TRY(check_rows(a->y, a->ldy, a->d_out));
-  if (a->y == a->x || a->y == a->w) return MLORA_ERR_SHAPE;
+  if (!apart(a->y, a->x, a->w, a->x_scale, a->w_scale)) return MLORA_ERR_SHAPE;
   if (!aligned(dev_status, 4)) return MLORA_ERR_ALIGN;
   return done(mlora::launch_fp8_matmul(*a, dev_status, mlora::api_wait_limit_ns(), static_cast<cudaStream_t>(stream)), "8-bit product launch");
 }
@@ -116,6 +126,9 @@ int lora_sample(const mlora_sampling *a, int32_t *dev_status, void *stream) {
       !all_aligned(4, a->row_request, a->uniform, a->temperature, a->top_k, a->top_p, a->min_p, a->token, a->logprob,
                    dev_status))
     return MLORA_ERR_ALIGN;
+  if (!apart(a->token, a->logits, a->row_request, a->uniform, a->temperature, a->top_k, a->top_p, a->min_p) ||
+      !apart(a->logprob, a->logits, a->row_request, a->uniform, a->temperature, a->top_k, a->top_p, a->min_p, a->token))
+    return MLORA_ERR_SHAPE;
   return done(mlora::launch_sample(*a, dev_status, static_cast<cudaStream_t>(stream)), "sampling launch");
 }
 

@@ -499,8 +499,8 @@ MLORA_API int lora_logits_adjust(const mlora_logits *args, int32_t *dev_status, 
  *   residual_out = round(h),   v = weight * h / sqrt(mean of h^2 over the row + eps),   out = round(v),
  *   (q, q_scale) = v as 8-bit rows,
  * in fp32 from the unrounded h, each output rounded once. residual and residual_out come together, and q and q_scale; out
- * or q may be NULL, not both. residual_out may be residual or x, and out may be x or residual, with equal leading dimensions; no two
- * outputs are the same array. Sums and squares may pass fp32's range: finite rows of x and residual have a
+ * or q may be NULL, not both. residual_out may be residual or x, and out may be x or residual, with equal leading dimensions; every
+ * other output is an array of its own. Sums and squares may pass fp32's range: finite rows of x and residual have a
  * finite norm (residual_out is rounded as any sum is). */
 typedef struct {
   int32_t num_rows, width, dtype; /* width a multiple of 8, 8 .. MLORA_ROW_MAX_WIDTH; dtype of x, residual, weight, out */
@@ -519,8 +519,8 @@ MLORA_API int lora_rms_norm(const mlora_norm *args, void *stream);
 
 /* lora_quantize: v = x, or x * gate / (1 + exp(-gate)) with a gate, in fp32;
  *   (q, q_scale) = v as 8-bit rows,   out = round(v)
- * q (with q_scale) or out may be NULL, not both. out may be x or gate, with equal leading dimensions. gate and x may be column blocks
- * of one array. 1 / (1 + exp(-gate)) is held to 2^-149. */
+ * q (with q_scale) or out may be NULL, not both. out may be x or gate, with equal leading dimensions; the other outputs are arrays
+ * of their own. gate and x may be column blocks of one array. 1 / (1 + exp(-gate)) is held to 2^-149. */
 typedef struct {
   int32_t num_rows, width, dtype; /* width a multiple of 8, at least 8; dtype of x, gate, out */
   const void *x;                  /* [num_rows][ldx] */
@@ -565,6 +565,7 @@ MLORA_API int lora_fp8_matmul(const mlora_matmul *args, int32_t *dev_status, voi
  * -inf gets token -1 and logprob -inf. uniform outside [0, 1) is taken to the nearer end, NaN as 0.
  * The sums are of whole numbers, 2^-44 of the largest w each (w to 2^-36 of itself, below 2^-18
  * of the largest to 2^-40 of that): the same bits on every call.
+ * token and logprob are arrays of their own.
  * Status: row_request[i] outside [-1, num_requests) (BAD_REQUEST): the row is skipped. */
 typedef struct {
   int32_t num_rows, vocab, dtype; /* 1 <= vocab <= MLORA_SAMPLE_MAX_VOCAB; dtype: MLORA_FP32, MLORA_BF16 or MLORA_FP16 */

@@ -22,3 +22,17 @@ def test_an_eps_below_fp32s_normal_numbers(L, eps):  # noqa: F811
     """Squares as small as such an eps have no 24 bits."""
     assert call(L, "norm", dict(eps=eps), NORM) == m.ERR_SHAPE
     assert call(L, "norm", dict(eps=2.0 ** -126, num_rows=0), NORM) == 0
+
+
+@pytest.mark.parametrize("name, base, out, others", [
+    ("norm", NORM, "q", ["x", "residual", "weight", "out", "residual_out"]),
+    ("norm", NORM, "q_scale", ["x", "residual", "weight", "out", "residual_out", "q"]),
+    ("norm", NORM, "out", ["weight", "residual_out"]), ("norm", NORM, "residual_out", ["weight"]),
+    ("quant", QUANT, "q", ["x", "gate", "out"]), ("quant", QUANT, "q_scale", ["x", "gate", "out", "q"]),
+    ("matmul", MATMUL, "y", ["x", "w", "x_scale", "w_scale"]),
+    ("sampling", SAMPLING, "token", ["logits", "row_request", "uniform", "temperature", "top_k", "top_p", "min_p"]),
+    ("sampling", SAMPLING, "logprob", ["logits", "row_request", "uniform", "temperature", "top_k", "top_p", "min_p", "token"])])
+def test_an_output_over_another_array(L, name, base, out, others):  # noqa: F811
+    """Other rows' CTAs would read what has been written."""
+    for other in others:
+        assert call(L, name, {out: base[other]}, base) == m.ERR_SHAPE, (out, other)

@@ -613,9 +613,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   } else {
     me.each([&](float v, int) { top = fmaxf(top, v); });
   }
-  const float temp = p.temperature ? p.temperature[r] : 1.f;
+  float temp = p.temperature ? p.temperature[r] : 1.f;
   int k = p.top_k ? p.top_k[r] : 0;
-  if (!(temp > 0.f)) k = 1;
+  if (temp > 0.f) temp = fmaxf(temp, 0x1p-126f);
+  else temp = 1.f, k = 1;
   const float limit = p.top_p ? p.top_p[r] : 1.f, least_p = p.min_p ? p.min_p[r] : 0.f;
   for (int i = tid; i < kExp2Steps; i += kThreads) sh.steps[i] = exp2_steps[i];
   for (int i = tid; i <= kBins; i += kThreads) sh.bins.count[i] = 0, sh.bins.mass[i] = 0;
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     cluster_sync();
     for (int c = 0; c < ctas; ++c) top = fmaxf(top, sh.top[c]);
   }
-  me.top = top, me.scale = weight_scale(temp > 0.f ? temp : 1.f);
+  me.top = top, me.scale = weight_scale(temp);
   const bool sum_all = k <= 0 && (limit < 1.f || !(least_p > 0.f));  // whether the limits begin with the sum of all weights
   const float range = k > 0 ? kRangeOfK : kRangeOfSum;
   const int near = (int)(kBins * kNear / range);

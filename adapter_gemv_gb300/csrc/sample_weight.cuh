@@ -41,15 +41,15 @@ __constant__ float2 exp2_steps[kExp2Steps] = {
     {0x1.6a09e6p0f, 0x1.9fcef4p-26f},
 };
 
-// log2(e) / T = hi + lo; 0 <= hi, finite
+// log2(e) / T = hi + lo, T from 2^-126 on: 0 <= hi < 2^127
 struct WeightScale {
   float hi, lo;
 };
 __device__ __forceinline__ WeightScale weight_scale(float temperature) {
   constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f;  // log2(e)
   WeightScale s;
-  s.hi = fminf(kHi / temperature, 3e38f);  // (there: every token below the largest has weight 0)
-  s.lo = s.hi < 3e38f ? (fmaf(-s.hi, temperature, kHi) + kLo) / temperature : 0.f;
+  s.hi = kHi / temperature;
+  s.lo = (fmaf(-s.hi, temperature, kHi) + kLo) / temperature;
   if (!(fabsf(s.lo) < 3e38f)) s.lo = 0.f;  // (an infinite temperature: every weight is 1)
   return s;
 }

@@ -559,8 +559,9 @@ MLORA_API int lora_fp8_matmul(const mlora_matmul *args, int32_t *dev_status, voi
  *   top_p[r] < 1:     the fewest whose w sum to at least top_p[r] times the sum over those that top_k leaves
  *   min_p[r] > 0:     the tokens with w_t >= min_p[r]
  * and at least one token; token[i] is the first of the order at which the running sum of w exceeds uniform[i] times the sum
- * over those kept, logprob[i] = log(its w / that sum). T <= 0: the first token of the order. Every array of the requests may be NULL and
- * then has no part (T = 1). Behind lora_logits_adjust, the temperature is given to one of the two calls.
+ * over those kept, logprob[i] = log(its w / that sum). T <= 0: the first token of the order; 0 < T < 2^-126 counts as
+ * 2^-126. A difference of logits beyond fp32's range has w = 0. Every array of the requests may be NULL and then has no
+ * part (T = 1). Behind lora_logits_adjust, the temperature is given to one of the two calls.
  * A NaN logit counts as -inf; -inf has w = 0; of logits of +inf each has w = 1 and all others 0. A row with nothing but
  * -inf gets token -1 and logprob -inf. uniform outside [0, 1) is taken to the nearer end, NaN as 0.
  * The sums are of whole numbers, 2^-44 of the largest w each (w to 2^-36 of itself, below 2^-18

@@ -590,23 +590,18 @@ cudaError_t dispatch(MatmulParams p, int32_t *status, cudaStream_t stream) {
 
 }  // namespace
 
+// Tiles of 16 rows by 128 are counted in 31 bits, eight times over.
+bool fp8_matmul_fits(const mlora_matmul &a) {
+  return ((a.num_rows - 1) / 16 + 1) * (int64_t)((a.d_out - 1) / kTile + 1) <= INT32_MAX / kMaxSplit;
+}
+
 cudaError_t launch_fp8_matmul(const mlora_matmul &a, int32_t *status, uint64_t wait_ns, cudaStream_t stream) {
-  // rows of a launch: tiles of 16 rows by 128 are counted in 31 bits, eight times over
-  const int64_t most = std::max<int64_t>(1, (INT32_MAX / kMaxSplit) / ((a.d_out - 1) / kTile + 1)) * 16;
-  for (int64_t row0 = 0; row0 < a.num_rows; row0 += most) {
-    MatmulParams p{};
-    p.a = a;
-    p.wait_ns = wait_ns ? wait_ns : kWaitLimitNs;
-    p.a.num_rows = (int32_t)std::min<int64_t>(most, a.num_rows - row0);
-    p.a.x = static_cast<const uint8_t *>(a.x) + row0 * a.ldx;
-    p.a.x_scale = a.x_scale + row0 * a.ldxs;
-    p.a.y = static_cast<uint16_t *>(a.y) + row0 * a.ldy;
-    const auto run = a.dtype == MLORA_BF16 ? (wait_ns ? dispatch<MLORA_BF16, true> : dispatch<MLORA_BF16, false>)
-                                           : (wait_ns ? dispatch<MLORA_FP16, true> : dispatch<MLORA_FP16, false>);
-    const cudaError_t e = run(p, status, stream);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  MatmulParams p{};
+  p.a = a;
+  p.wait_ns = wait_ns ? wait_ns : kWaitLimitNs;
+  const auto run = a.dtype == MLORA_BF16 ? (wait_ns ? dispatch<MLORA_BF16, true> : dispatch<MLORA_BF16, false>)
+                                         : (wait_ns ? dispatch<MLORA_FP16, true> : dispatch<MLORA_FP16, false>);
+  return run(p, status, stream);
 }
 
 }  // namespace mlora

@@ -26,6 +26,7 @@ cudaError_t launch_logits_adjust(const mlora_logits &a, int32_t *status, cudaStr
 cudaError_t launch_rms_norm(const mlora_norm &a, cudaStream_t stream);
 cudaError_t launch_quantize(const mlora_quant &a, cudaStream_t stream);
 cudaError_t launch_fp8_matmul(const mlora_matmul &a, int32_t *status, uint64_t wait_ns, cudaStream_t stream);
+bool fp8_matmul_fits(const mlora_matmul &a);  // its tiles counted in 31 bits
 cudaError_t launch_sample(const mlora_sampling &a, int32_t *status, cudaStream_t stream);
 
 // Defined in decode_launch.cu: number of SMs of the current device.

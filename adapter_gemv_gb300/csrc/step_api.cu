@@ -104,6 +104,7 @@ int lora_fp8_matmul(const mlora_matmul *a, int32_t *dev_status, void *stream) {
   if (a->d_out > INT32_MAX - 256) return MLORA_ERR_SHAPE;  // a tile's last column is counted in 31 bits
   if (a->d_in % 16 || a->d_out % 8) return MLORA_ERR_ALIGN;
   if (a->num_rows == 0) return MLORA_OK;
+  if (!mlora::fp8_matmul_fits(*a)) return MLORA_ERR_SHAPE;
   const int64_t blocks = blocks_of(a->d_in);
   TRY(check_bytes(a->x, a->ldx, a->d_in, 16));
   TRY(check_bytes(a->w, a->ldw, a->d_in, 16));

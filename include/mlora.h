@@ -541,7 +541,8 @@ MLORA_API int lora_quantize(const mlora_quant *args, void *stream);
  * fp32, whose range their product must not leave. y is no other array.
  * TIMEOUT as for the adapters' calls. */
 typedef struct {
-  int32_t num_rows, d_in, d_out, dtype; /* d_in a multiple of 16, d_out of 8 and below 2^31 - 256 */
+  int32_t num_rows, d_in, d_out, dtype; /* d_in a multiple of 16, d_out of 8 and below 2^31 - 256;
+                                           ceil(num_rows / 16) ceil(d_out / 128) below 2^28 */
   const void *x;                        /* [num_rows][ldx], ldx a multiple of 16 */
   const float *x_scale;                 /* [num_rows][ldxs >= ceil(d_in / 128)] */
   const void *w;                        /* [d_out][ldw], ldw a multiple of 16 */

@@ -36,3 +36,9 @@ def test_an_output_over_another_array(L, name, base, out, others):  # noqa: F811
     """Other rows' CTAs would read what has been written."""
     for other in others:
         assert call(L, name, {out: base[other]}, base) == m.ERR_SHAPE, (out, other)
+
+
+@pytest.mark.parametrize("num_rows, d_out", [(2 ** 31 - 1, 264), (2 ** 28 + 1, 2048), (2 ** 20, 2 ** 20)])
+def test_a_product_of_more_tiles_than_a_grid_counts(L, num_rows, d_out):  # noqa: F811
+    """(y would be a terabyte or more)"""
+    assert call(L, "matmul", dict(num_rows=num_rows, d_out=d_out, ldy=d_out), MATMUL) == m.ERR_SHAPE

@@ -86,3 +86,34 @@ def test_scales_of_all_sizes(dev):  # noqa: F811
     amax = x.cpu().float().abs().amax(1, keepdim=True)
     assert torch.equal(scale.cpu(), torch.maximum(amax / torch.full_like(amax, 448), torch.tensor(2.0 ** -126)))
     assert torch.equal(q.cpu().float(), quotients(x, scale).float())
+
+
+# silu(gate) x in fp32: expf is documented to 1 ulp, at most 2 u of its value. A negative gate: its product with that 3 u, 1 + exp 2 u at
+# most, the quotient 1 u, the product with x 1 u: 7 u, and a little for their products. A positive one: 4 u.
+GATED = 7.001 * ref.U
+
+
+@pytest.mark.parametrize("dtype, std", [(FP16, 4.0), (BF16, 1.5), (BF16, 12.0)])
+def test_gated_values_are_off_by_a_few_roundings(dev, dtype, std):  # noqa: F811
+    """Whatever the gate's size, in 16 bits and in 8: no value is rounded the wrong way that is further than that from
+    the border between its neighbours."""
+    rows, width = 2048, 8192
+    x, g = normal((rows, width), dtype, dev, 31, 1.5), normal((rows, width), dtype, dev, 32, std)
+    out, q = torch.empty_like(x), torch.empty_like(x, dtype=ref.E4M3)
+    scale = torch.empty((rows, width // 128), device=dev)
+    m.lora_quantize(x, q, scale, gate=g, out=out)
+    v = x.double() * g.double() / (1 + torch.exp(-g.double()))
+    bits = {BF16: 8, FP16: 11}[dtype]
+    half = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=torch.finfo(dtype).tiny))) - bits)
+    bound = half + v.abs() * GATED
+    off = (out.double() - v).abs()
+    assert bool((off <= bound).all()), f"{int((off > bound).sum())} of out off, worst {float((off / bound).max()):.6f}"
+    blocks = v.reshape(rows, -1, 128)
+    amax = torch.maximum(blocks.abs().amax(-1) / 448, torch.full_like(scale, 2.0 ** -126, dtype=torch.float64))
+    assert bool(((scale.double() - amax).abs() <= amax * (GATED + ref.U)).all())
+    z = (blocks / scale.double()[..., None]).reshape(rows, width)
+    off = (q.double() - z).abs()
+    half = torch.exp2(torch.floor(torch.log2(z.abs().clamp(min=2.0 ** -6))) - 4)
+    # (the values' error, the quotient's rounding; behind the largest of a binade the next one's step begins)
+    bound = half + z.abs() * (GATED + 1.001 * ref.U)
+    assert bool((off <= bound).all()), f"{int((off > bound).sum())} of q off, worst {float((off / bound).max()):.6f}"

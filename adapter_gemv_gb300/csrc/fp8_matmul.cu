@@ -9,12 +9,14 @@
 //
 // Few rows: W is read once, from memory, and that bounds. W's rows are the MMA's 128, x's its 16, 32 or 64 columns, so a product
 // is read back with 16 to 64 values a lane. The K blocks of a tile are split over a cluster of up to 8 CTAs, which add
-// their sums through distributed shared memory in rank order. 32 x 4096 x 22016 (92 MB): 17.7 us, 5.2 TB/s (20 SMs of 152
-// have two tiles); 8 x 8192 x 28672 37.6 us, 6.3 TB/s; 1 x 4096 x 4096 5.7 us.
+// their sums through distributed shared memory in rank order. 32 x 4096 x 22016 (92 MB): 17.8 us, 5.2 TB/s (20 SMs of 152
+// have two tiles); 8 x 8192 x 28672 38.0 us, 6.2 TB/s; 1 x 4096 x 4096 5.8 us.
 //
-// Many rows: 128 of x by up to 256 of W, one persistent CTA an SM. 12604 x 5120 x 13824: 808 to 823 us, 2.2 PFLOP/s; bound by the
-// sums: a tile's block is 32768 of them, 256 cycles of the SM's FMA units at least, and with the reads from TMEM, the scales and the
-// turns of the two accumulators 1000, where its MMAs take 512. Tried on 7680 x 8192 x 7680 (353 us): a pair of CTAs on 256 rows
+// Many rows: 128 of x by up to 256 of W, one persistent CTA an SM. 12604 x 5120 x 13824: 815 to 835 us, 2.15 PFLOP/s. Bound by the
+// length of a turn: a tile's block is 32768 sums, 256 cycles of the SM's FMA units, and its MMAs take 512 in the other accumulator
+// meanwhile, but a turn takes 1000: a warp reads its part of TMEM 8 columns at a time, eight trips one behind the other, with one
+// on its way at any moment. (2048 x 4096 x 11008 under ncu: tensor cores 41 % busy, FMA units 25 %, schedulers 59 %; most stalls
+// are such waits.) Tried on 7680 x 8192 x 7680 (353 us then, 375 to 410 by the card's clock): a pair of CTAs on 256 rows
 // (cta_group::2, half the loads of W) 4 % slower; four accumulators of 128 columns 17 %; the next turn's barrier polled
 // early 6 %; loads of 16 and 32 columns at a time spill and are slower.
 #include <cuda.h>
@@ -563,7 +565,7 @@ template <int DT, bool SHORT>
 cudaError_t dispatch(MatmulParams p, int32_t *status, cudaStream_t stream) {
   const int rows = p.a.num_rows, sms = sm_count();
   p.blocks = (p.a.d_in - 1) / kBlock + 1;
-  // Few rows where its tiles (and there are up to 64 rows in one) leave no SM two of them: 128 x 4096 x 4096 9.8 us against 15.8,
+  // Few rows where its tiles (and there are up to 64 rows in one) leave no SM two of them: 128 x 4096 x 4096 10.0 us against 15.8,
   // 512 x 4096 x 1024 9.9 against 16.1; 213 x 8192 x 8192, 256 tiles: 33 against 30. And up to 64 rows in any case: 64 x 8192 x
   // 28672 42.3 against 41.5, 64 x 4096 x 11008 14.1 against 17.0.
   const int nt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;

@@ -1,9 +1,11 @@
 // quantize.cu -- 16-bit rows, or silu(gate) x of an MLP, as 8-bit rows (sm_103a).
 //
 // Elementwise but for the maximum of each block of 128, which half a warp holds: every element read once and
-// written once, bound by memory; by launch and one load for a decode step's rows. silu(gate) x of 12604 x 13824 with 16 and 8
-// bits out: 279 us, 4.4 TB/s. With __expf and __fdividef it took 205, with expf and __fdividef 225, but more values went to the wrong one of two e4m3
-// neighbours than with fp32's exponential and quotient.
+// written once; by launch and one load for a decode step's rows. Without a gate, 12604 x 4096 bf16 (157 MB): 40 us, bound by each thread's one
+// trip to memory (of 15 cycles a warp and instruction 7 wait for it, at six CTAs an SM by 34 registers). silu(gate) x of 12604 x 13824
+// with 16 and 8 bits out: 278 to 282 us, 4.4 TB/s, the schedulers 74 % busy with the exponential and the quotient, and the same trip. With
+// __expf and __fdividef it takes 209 us, with expf and __fdividef 231: of 174 M values the 8-bit ones are as good (328 and 326 at the wrong neighbour, 334 with
+// fp32's own exponential and quotient), but 470 and 461 of the 16-bit ones are rounded the wrong way, against 77 so and 123 of a plain fp32 form.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

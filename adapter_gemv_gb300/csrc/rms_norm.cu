@@ -5,7 +5,7 @@
 // memory for a prompt's rows, by launch, one load and the row's sum for a decode step's.
 //
 // A CTA takes a row, a thread chunks of 8 elements, CTA width apart: the 16 lanes of half a warp hold a block of
-// the 8-bit rows. 12604 rows of 5120 with a residual, 16 and 8 bits out (9 bytes an element): 110 us, 5.3 TB/s; 32 x 4096: 2.4 us.
+// the 8-bit rows. 12604 rows of 5120 with a residual, 16 and 8 bits out (9 bytes an element): 112 us, 5.2 TB/s; 32 x 4096: 2.5 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -116,7 +116,7 @@ cudaError_t launch(const mlora_norm &p, int threads, cudaStream_t stream) {
 template <int DT>
 cudaError_t dispatch(const mlora_norm &p, cudaStream_t stream) {
   const int chunks = p.width / 8;
-  // One chunk a thread as far as a CTA goes: 12604 x 5120 take 110 us so, 118 with two, 129 with four; 32 x 4096 2.4, 3.3, 5.0
+  // One chunk a thread as far as a CTA goes: 12604 x 5120 take 112 us so, 121 with two, 133 with four; 32 x 4096 2.5, 3.5, 5.2
   const int ch = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
   const int threads = ((chunks + ch - 1) / ch + 31) & ~31;
   if (ch == 1) return launch<DT, 1>(p, threads, stream);
